@@ -428,6 +428,116 @@ GPTQ_API int gptq_residual_add(const void* X, const float* Y, int64_t count, voi
                                void* stream);
 
 /*
+ * A decoder block's attention half, for the sequential pipeline (the calibration forward
+ * of quantized blocks) and for decoding single tokens beside gptq_qmatvec.  Activations are
+ * token-major here: [tokens, features] with contiguous features.  Types F32, F16, BF16
+ * where "any" is said.  tokens, count or total_q of 0 is a no-op.  d_status may be NULL.
+ *
+ * gptq_add_norm - the norms around a block with the residual addition between them:
+ *     Xn = round(X + alpha . gate . N(Y; post_weight, post_bias))      h = round(N(Xn; weight, bias))
+ *   N(v; w, b) = v / sqrt(mean(v^2) + eps) . w + b (RMS), of v - mean(v) with center != 0
+ *   (layer norm); b NULL: none; post_weight NULL: N(Y) is Y itself; gate NULL: 1.  Y NULL:
+ *   h = N(X) alone (Xn is not written and may be NULL).  h is taken from the rounded Xn.
+ *   X, Xn, h   x_dtype [tokens, d], row strides ld_x, ld_xn, ld_h (>= d).  Xn may be X
+ *              (same stride); other overlaps of outputs with inputs are not allowed.
+ *   Y          y_dtype [tokens, d], row stride ld_y.
+ *   weights, biases   p_dtype [d].  gate: p_dtype, [d] with ld_gate 0, or [tokens, d] with
+ *              row stride ld_gate (>= d).
+ *   1 <= d <= 32768 (GPTQ_ERR_UNSUPPORTED above: a row is held in one block's registers).
+ *   Statistics in fp32.  Rows of 16-byte multiples that start on 16 bytes are read fastest.
+ *
+ * gptq_rope_qkv - a product of stacked q, k and v layers, X [tokens, (heads_q + 2 heads_kv) .
+ *   head_dim] (any type, row stride ld), plus bias (fp32, NULL: none), split into q [tokens,
+ *   heads_q, head_dim], k and v [tokens, heads_kv, head_dim] (contiguous, out_dtype F16 or
+ *   BF16, rounded once); the first rot features of each q and k head turn by the angles of the
+ *   token's position: pair (a, b) -> (a cos - b sin, a sin + b cos), pairs (i, i + rot/2) or,
+ *   interleaved != 0, (2i, 2i + 1).
+ *   cos, sin   fp32 [max_pos, rot/2].  rot even, 0 (no rotation; tables may be NULL) to head_dim.
+ *   positions  int32 [tokens], NULL: token t is at position t.  A position outside
+ *              [0, max_pos) is recorded (GPTQ_ERR_INVALID_ARG, info = token) and read as 0.
+ *   head_dim even.
+ *
+ * gptq_attention - softmax(scale . q k^T) v for the sequences of a packed batch.  Sequence b has
+ *   queries cu_q[b] .. cu_q[b+1]-1 (rows of q and o) and keys cu_k[b] .. cu_k[b+1]-1 (rows of k
+ *   and v), any lengths, 0 included.  Query i of a sequence sees every key, or with causal != 0
+ *   keys 0 .. i + Lk - Lq (the last query sees the last key; with Lk > Lq the first Lk - Lq
+ *   keys precede the queries).  A query that sees no key gives 0.  Keys a query does not see take
+ *   no part in its result, whatever their rows hold (NaN and infinities included).
+ *   q, o       dtype (F16 or BF16) [total_q, heads_q, head_dim]; k, v [total_k, heads_kv,
+ *              head_dim]; token and head strides in elements, features contiguous, pointers
+ *              16-byte aligned, strides multiples of 8.  Query head h reads k/v head
+ *              h / (heads_q / heads_kv).
+ *   cu_q, cu_k int32 [count + 1], on the device, non-decreasing, within [0, total].  A sequence
+ *              whose bounds are not is recorded (GPTQ_ERR_INVALID_ARG, info = b) and skipped.
+ *              Rows of o outside every sequence are left as they were.
+ *   head_dim   a multiple of 8, 8 to 128.  o must not overlap q, k or v.
+ *   Sums and statistics in fp32; the weights are rounded to dtype for the product with v.
+ *
+ * The cache of keys and values in 4 bits.  Every group of `group` consecutive features of a
+ * head of one token has an fp16 scale s and an integer zero point z in fp16, chosen as
+ * gptq_quantize_layer chooses an asymmetric group's; codes 0 .. 15, value s . (code - z).
+ *   k_codes, v_codes    int32 [pages, heads, page_size, head_dim/8]: feature f in bits
+ *                       4 (f mod 8) of word f / 8
+ *   k_params, v_params  fp16 (as uint16) [pages, heads, page_size, head_dim/group, 2]: s, z
+ *   head_dim 64 or 128; group 32, 64 or 128, at most head_dim; page_size a power of two, 16
+ *   to 1024; all pointers 16-byte aligned.
+ * table int32 [count, width] names the pages of each sequence in order: position p of sequence
+ * b lies in page table[b][p / page_size], row p mod page_size.
+ *
+ * gptq_kv4_append - token t of k and v (dtype F16 or BF16, [tokens, heads, head_dim], strides as
+ *   gptq_attention's) with cu[b] <= t < cu[b+1] goes to position start[b] + t - cu[b] of sequence
+ *   b; tokens outside every sequence are skipped.  A position that the table does not hold is
+ *   recorded (GPTQ_ERR_INVALID_ARG, info = t) and skipped.  A group with a NaN or an infinity is
+ *   recorded (GPTQ_ERR_NONFINITE, info = t) and reads back as NaN.  Every position must be written
+ *   by one token only (a page shared by two sequences is read-only for both).
+ * gptq_kv4_read - the inverse: k and v (any dtype, [tokens, heads, head_dim] contiguous) from
+ *   the positions start[b] + t - cu[b] (start NULL: 0); rounded once.
+ * gptq_kv4_attention - one query per sequence: o[b] = softmax(scale . q[b] k^T) v over positions
+ *   0 .. lengths[b] - 1 of sequence b (lengths int32 [count] on the device; 0 gives 0).  q, o dtype
+ *   (F16 or BF16) [count, heads_q, head_dim], strides as above.  A length below 0 or beyond
+ *   width . page_size is recorded (GPTQ_ERR_INVALID_ARG, info = b) and that row of o is left as
+ *   it was; a table entry that names no page is recorded the same way and its tokens take no part.
+ *   ws >= gptq_kv4_attention_workspace_size(...) bytes, 256-byte aligned; calls that may run at the
+ *   same time (two graphs on two streams) need one each.  Deterministic.
+ */
+typedef struct {
+  int32_t* k_codes;
+  uint16_t* k_params;
+  int32_t* v_codes;
+  uint16_t* v_params;
+  int pages, page_size, heads, head_dim, group;
+} gptq_kv4_cache;
+
+GPTQ_API int gptq_add_norm(const void* X, int x_dtype, int64_t ld_x, const void* Y, int y_dtype, int64_t ld_y,
+                           const void* weight, const void* bias, const void* post_weight, const void* post_bias,
+                           const void* gate, int64_t ld_gate, int p_dtype, int tokens, int d, float alpha, float eps,
+                           int center, void* Xn, int64_t ld_xn, void* h, int64_t ld_h, int32_t* d_status,
+                           void* stream);
+GPTQ_API int gptq_rope_qkv(const void* X, int x_dtype, int64_t ld, const float* bias, const float* cos,
+                           const float* sin, int max_pos, int rot, int interleaved, const int32_t* positions,
+                           int tokens, int heads_q, int heads_kv, int head_dim, int out_dtype, void* q, void* k,
+                           void* v, int32_t* d_status, void* stream);
+GPTQ_API int gptq_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                            int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                            int64_t v_head_stride, int dtype, const int32_t* cu_q, const int32_t* cu_k, int count,
+                            int total_q, int total_k, int heads_q, int heads_kv, int head_dim, float scale,
+                            int causal, void* o, int64_t o_token_stride, int64_t o_head_stride, int32_t* d_status,
+                            void* stream);
+GPTQ_API int gptq_kv4_append(const gptq_kv4_cache* cache, const void* k, int64_t k_token_stride,
+                             int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                             int dtype, int tokens, const int32_t* table, int width, const int32_t* cu,
+                             const int32_t* start, int count, int32_t* d_status, void* stream);
+GPTQ_API int gptq_kv4_read(const gptq_kv4_cache* cache, const int32_t* table, int width, const int32_t* cu,
+                           const int32_t* start, int count, int tokens, int dtype, void* k, void* v,
+                           int32_t* d_status, void* stream);
+GPTQ_API size_t gptq_kv4_attention_workspace_size(int count, int heads_q, int heads_kv, int head_dim, int width,
+                                                  int page_size);
+GPTQ_API int gptq_kv4_attention(const gptq_kv4_cache* cache, const void* q, int64_t q_token_stride,
+                                int64_t q_head_stride, int dtype, int count, int heads_q, const int32_t* table,
+                                int width, const int32_t* lengths, float scale, void* o, int64_t o_token_stride,
+                                int64_t o_head_stride, void* ws, size_t ws_bytes, int32_t* d_status, void* stream);
+
+/*
  * Kernel timing trace.  The GPTQ pages have no counterpart to these calls: they
  * are a measurement aid.  While the trace is on, every kernel the library launches
  * is bracketed by two CUDA events recorded on the stream it is launched on (the

@@ -1,0 +1,383 @@
+"""The attention half of a decoder block: argument marshalling only, as in gptq.py.
+
+    add_norm(X, weight, Y, ...)                  -> (Xn, h)    norms around a block, residual, gate
+    rope_qkv(QKV, cos, sin, heads_q, heads_kv, head_dim, ...)  -> (q, k, v)
+    attention(q, k, v, cu_q, cu_k, causal)       -> o          packed prompts, grouped heads
+    kv4_alloc(pages, page_size, heads, head_dim, group) -> KV4Cache   keys and values in 4 bits
+    kv4_append(cache, k, v, table, cu, start)    tokens into the cache
+    kv4_read(cache, table, cu, tokens, start)    -> (k, v)     and back
+    kv4_attention(q, cache, table, lengths)      -> o          one token per sequence
+
+include/gptq.h holds the formulas, the layouts and what is recorded in the status block.
+All tensors of a call are on one device, which need not be the current one.  stream: the
+stream to launch on (default: that device's current stream); the caller orders it with the
+streams that made the inputs.  What a call allocates belongs to the stream it launches on.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import dataclasses
+from typing import Optional, Tuple
+
+import torch
+
+from .gptq import _DTYPE_CODE, _KV4, _check, _ptr, _require_cuda, lib, workspace
+
+_16BIT = (torch.float16, torch.bfloat16)
+
+
+@contextlib.contextmanager
+def _launching(stream, *ts: Optional[torch.Tensor]):
+    """The call's device made current, and its stream (as a pointer); allocations go to that stream."""
+    _require_cuda(*ts)
+    dev = next(t.device for t in ts if t is not None)
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError("all tensors must be on one device")
+    if stream is None:
+        if dev.index == torch.cuda.current_device():
+            yield ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+            return
+        with torch.cuda.device(dev):
+            yield ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+        return
+    if stream.device != dev:
+        raise ValueError("stream must be on the tensors' device")
+    with torch.cuda.stream(stream):
+        yield ctypes.c_void_p(stream.cuda_stream)
+
+
+def _status_ok(status: Optional[torch.Tensor]):
+    if status is not None and (status.dtype != torch.int32 or status.numel() != 4 or not status.is_contiguous()):
+        raise ValueError("status must be a contiguous int32 [4] tensor")
+
+
+def _span(t: torch.Tensor):
+    """First and last byte of a tensor's elements (end exclusive)."""
+    if t.numel() == 0:
+        return t.data_ptr(), t.data_ptr()
+    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
+
+def _apart(out: Optional[torch.Tensor], *ins: Optional[torch.Tensor]):
+    """Raise if out's memory overlaps an input's."""
+    if out is None or out.numel() == 0:
+        return
+    a0, a1 = _span(out)
+    for t in ins:
+        if t is not None and t.numel() > 0 and t.device == out.device:
+            b0, b1 = _span(t)
+            if a0 < b1 and b0 < a1:
+                raise ValueError("an output overlaps an input")
+
+
+def _rows(t: torch.Tensor, tokens: int, d: int, what: str):
+    if t.dim() != 2 or tuple(t.shape) != (tokens, d) or t.dtype not in _DTYPE_CODE or (d > 1 and t.stride(1) != 1) \
+            or (tokens > 1 and t.stride(0) < d):
+        raise ValueError(f"{what} must be an fp32/fp16/bf16 [{tokens}, {d}] tensor with contiguous rows")
+
+
+def _ld(t: Optional[torch.Tensor], d: int) -> int:
+    """Row stride; that of a single row is not used (torch may report any)."""
+    return d if t is None or t.shape[0] <= 1 else t.stride(0)
+
+
+def _ints(t: torch.Tensor, shape, what: str):
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)}")
+
+
+# --------------------------------------------------------------------------- #
+# The residual stream
+# --------------------------------------------------------------------------- #
+def add_norm(X: torch.Tensor, weight: torch.Tensor, Y: Optional[torch.Tensor] = None,
+             post_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, alpha: float = 1.0,
+             eps: float = 1e-6, center: bool = False, bias: Optional[torch.Tensor] = None,
+             post_bias: Optional[torch.Tensor] = None, x_out: Optional[torch.Tensor] = None,
+             out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+             stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(Xn, h): Xn = X + alpha . gate . N(Y; post_weight, post_bias), h = N(Xn; weight, bias).
+
+    N is the RMS norm, or with center the layer norm; without post_weight N(Y) is Y, without Y
+    Xn is X itself.  X [tokens, d] and Y [tokens, d] fp32/fp16/bf16; weights, biases [d] and
+    gate [d] or [tokens, d] of one of those types.  x_out may be X (the stream updated in place).
+    """
+    if X.dim() != 2:
+        raise ValueError("X must be a [tokens, d] tensor")
+    tokens, d = X.shape
+    _rows(X, tokens, d, "X")
+    if Y is None and (post_weight is not None or gate is not None or x_out is not None):
+        raise ValueError("post_weight, gate and x_out belong to Y")
+    if post_bias is not None and post_weight is None:
+        raise ValueError("post_bias belongs to post_weight")
+    if Y is not None:
+        _rows(Y, tokens, d, "Y")
+    if weight.dtype not in _DTYPE_CODE:
+        raise ValueError("weight must be fp32/fp16/bf16")
+    for t, what in ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight"), (post_bias, "post_bias")):
+        if t is not None and (tuple(t.shape) != (d,) or t.dtype != weight.dtype or not t.is_contiguous()):
+            raise ValueError(f"{what} must be a contiguous [{d}] tensor of weight's type")
+    ld_gate = 0
+    if gate is not None:
+        if gate.dtype != weight.dtype:
+            raise ValueError("gate must have weight's type")
+        if gate.dim() == 2:
+            _rows(gate, tokens, d, "gate")
+            ld_gate = _ld(gate, d)
+        elif tuple(gate.shape) != (d,) or not gate.is_contiguous():
+            raise ValueError(f"gate must be a contiguous [{d}] or a [{tokens}, {d}] tensor")
+    _status_ok(status)
+    with _launching(stream, X, weight, Y, post_weight, gate, bias, post_bias, x_out, out, status) as s:
+        if out is None:
+            out = torch.empty((tokens, d), dtype=X.dtype, device=X.device)
+        if Y is not None and x_out is None:
+            x_out = torch.empty((tokens, d), dtype=X.dtype, device=X.device)
+        for t, what in ((out, "out"), (x_out, "x_out")):
+            if t is not None:
+                _rows(t, tokens, d, what)
+                if t.dtype != X.dtype:
+                    raise ValueError(f"{what} must have X's type")
+        par = (weight, bias, post_weight, post_bias, gate)
+        _apart(out, X, Y, x_out, *par)
+        same = x_out is not None and x_out.data_ptr() == X.data_ptr() and _ld(x_out, d) == _ld(X, d)
+        _apart(x_out, None if same else X, Y, *par)
+        _check(lib().gptq_add_norm(_ptr(X), _DTYPE_CODE[X.dtype], _ld(X, d), _ptr(Y),
+                                   _DTYPE_CODE[Y.dtype if Y is not None else X.dtype], _ld(Y, d), _ptr(weight),
+                                   _ptr(bias), _ptr(post_weight), _ptr(post_bias), _ptr(gate), ld_gate,
+                                   _DTYPE_CODE[weight.dtype], tokens, d, float(alpha), float(eps), int(bool(center)),
+                                   _ptr(x_out), _ld(x_out, d), _ptr(out), _ld(out, d), _ptr(status), s),
+               "gptq_add_norm")
+    return (X if Y is None else x_out), out
+
+
+def rope_qkv(QKV: torch.Tensor, cos: Optional[torch.Tensor], sin: Optional[torch.Tensor], heads_q: int, heads_kv: int,
+             head_dim: int, positions: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+             interleaved: bool = False, dtype=torch.bfloat16, status: Optional[torch.Tensor] = None,
+             stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(q, k, v) from the product of the stacked q, k and v layers, q and k rotated by position.
+
+    QKV [tokens, (heads_q + 2 heads_kv) head_dim] fp32/fp16/bf16; bias fp32; cos, sin fp32
+    [positions, rot / 2] (None: no rotation); positions int32 [tokens] (None: 0, 1, ...).
+    """
+    heads_q, heads_kv, head_dim = int(heads_q), int(heads_kv), int(head_dim)
+    cols = (heads_q + 2 * heads_kv) * head_dim
+    if heads_q < 1 or heads_kv < 1 or head_dim < 2 or QKV.dim() != 2:
+        raise ValueError("QKV must be a [tokens, (heads_q + 2 heads_kv) head_dim] tensor")
+    tokens = QKV.shape[0]
+    _rows(QKV, tokens, cols, "QKV")
+    if dtype not in _16BIT:
+        raise ValueError("dtype must be float16 or bfloat16")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    rot = max_pos = 0
+    if cos is not None:
+        for t in (cos, sin):
+            if t.dtype != torch.float32 or t.dim() != 2 or t.shape != cos.shape or not t.is_contiguous():
+                raise ValueError("cos and sin must be contiguous fp32 [positions, rot / 2] tensors of one shape")
+        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (cols,) or not bias.is_contiguous()):
+        raise ValueError(f"bias must be a contiguous fp32 [{cols}] tensor")
+    if positions is not None:
+        _ints(positions, (tokens,), "positions")
+    _status_ok(status)
+    with _launching(stream, QKV, cos, sin, positions, bias, status) as s:
+        q = torch.empty((tokens, heads_q, head_dim), dtype=dtype, device=QKV.device)
+        k = torch.empty((tokens, heads_kv, head_dim), dtype=dtype, device=QKV.device)
+        v = torch.empty((tokens, heads_kv, head_dim), dtype=dtype, device=QKV.device)
+        _check(lib().gptq_rope_qkv(_ptr(QKV), _DTYPE_CODE[QKV.dtype], _ld(QKV, cols), _ptr(bias), _ptr(cos),
+                                   _ptr(sin), max_pos, rot, int(bool(interleaved)), _ptr(positions), tokens, heads_q,
+                                   heads_kv, head_dim, _DTYPE_CODE[dtype], _ptr(q), _ptr(k), _ptr(v), _ptr(status),
+                                   s), "gptq_rope_qkv")
+    return q, k, v
+
+
+# --------------------------------------------------------------------------- #
+# Attention over packed prompts
+# --------------------------------------------------------------------------- #
+def _heads(t: torch.Tensor, dtype, what: str):
+    if t.dim() != 3 or t.dtype != dtype or t.shape[1] < 1 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{what} must be a [tokens, heads, head_dim] tensor of type {dtype} with contiguous features")
+
+
+def _strides(t: torch.Tensor):
+    """Token and head strides; those of a single token or head are not used."""
+    n, h, d = t.shape
+    hs = t.stride(1) if h > 1 else d
+    return (t.stride(0) if n > 1 else h * hs), hs
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+              cu_k: Optional[torch.Tensor] = None, causal: bool = True, scale: Optional[float] = None,
+              out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """o = softmax(scale q k^T) v over the sequences of a packed batch.
+
+    q [total_q, heads_q, head_dim], k and v [total_k, heads_kv, head_dim], fp16 or bf16; cu_q and
+    cu_k int32 [sequences + 1], the first row of each sequence and the end (cu_k None: cu_q).
+    causal: the last query of a sequence sees its last key.  scale None: 1 / sqrt(head_dim).
+    Rows of o that belong to no sequence are not written.
+    """
+    if q.dtype not in _16BIT:
+        raise ValueError("q must be fp16 or bf16")
+    for t, what in ((q, "q"), (k, "k"), (v, "v")):
+        _heads(t, q.dtype, what)
+    hq, d = q.shape[1], q.shape[2]
+    hk = k.shape[1]
+    if k.shape != v.shape or k.shape[2] != d or hq % hk != 0:
+        raise ValueError("k and v must have one shape, q's head size, and a number of heads that divides q's")
+    cu_k = cu_q if cu_k is None else cu_k
+    if cu_q.dim() != 1 or cu_q.numel() < 1:
+        raise ValueError("cu_q must be int32 [sequences + 1]")
+    _ints(cu_q, cu_q.shape, "cu_q")
+    _ints(cu_k, cu_q.shape, "cu_k")
+    _status_ok(status)
+    with _launching(stream, q, k, v, cu_q, cu_k, out, status) as s:
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        _heads(out, q.dtype, "out")
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        _apart(out, q, k, v)
+        _check(lib().gptq_attention(_ptr(q), *_strides(q), _ptr(k), *_strides(k), _ptr(v), *_strides(v),
+                                    _DTYPE_CODE[q.dtype], _ptr(cu_q), _ptr(cu_k), cu_q.numel() - 1, q.shape[0],
+                                    k.shape[0], hq, hk, d, float(d ** -0.5 if scale is None else scale),
+                                    int(bool(causal)), _ptr(out), *_strides(out), _ptr(status), s), "gptq_attention")
+    return out
+
+
+# --------------------------------------------------------------------------- #
+# The cache in 4 bits
+# --------------------------------------------------------------------------- #
+@dataclasses.dataclass
+class KV4Cache:
+    k_codes: torch.Tensor    # int32 [pages, heads, page_size, head_dim / 8]
+    k_params: torch.Tensor   # fp16 [pages, heads, page_size, head_dim / group, 2]: scale, zero point
+    v_codes: torch.Tensor
+    v_params: torch.Tensor
+    group: int
+
+
+def kv4_alloc(pages: int, page_size: int, heads: int, head_dim: int, group: int = 128, device="cuda") -> KV4Cache:
+    """An empty cache (every value 0)."""
+    t = [torch.zeros(*s, dtype=dt, device=device)
+         for _ in range(2) for s, dt in (((pages, heads, page_size, head_dim // 8), torch.int32),
+                                         ((pages, heads, page_size, head_dim // group, 2), torch.float16))]
+    return KV4Cache(*t, group=int(group))
+
+
+def _cache(c: KV4Cache) -> _KV4:
+    if c.k_codes.dim() != 4:
+        raise ValueError("k_codes must be int32 [pages, heads, page_size, head_dim / 8]")
+    pages, heads, page, words = c.k_codes.shape
+    d = words * 8
+    if c.group < 1 or d % c.group:
+        raise ValueError("group must divide head_dim")
+    for codes, par in ((c.k_codes, c.k_params), (c.v_codes, c.v_params)):
+        if codes.dtype != torch.int32 or codes.shape != c.k_codes.shape or not codes.is_contiguous():
+            raise ValueError("codes must be contiguous int32 tensors of one shape")
+        if par.dtype != torch.float16 or tuple(par.shape) != (pages, heads, page, d // c.group, 2) \
+                or not par.is_contiguous():
+            raise ValueError("params must be contiguous fp16 [pages, heads, page_size, head_dim / group, 2] tensors")
+    return _KV4(c.k_codes.data_ptr(), c.k_params.data_ptr(), c.v_codes.data_ptr(), c.v_params.data_ptr(), pages, page,
+                heads, d, int(c.group))
+
+
+def _table(table: torch.Tensor, count: int):
+    if table.dim() != 2 or table.shape[0] != count:
+        raise ValueError("table must be int32 [sequences, pages of a sequence]")
+    _ints(table, table.shape, "table")
+
+
+def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, cu: torch.Tensor,
+               start: torch.Tensor, status: Optional[torch.Tensor] = None, stream=None) -> KV4Cache:
+    """Tokens' keys and values into the cache: row t of k and v, cu[b] <= t < cu[b + 1], goes to
+    position start[b] + t - cu[b] of sequence b, which lies in page table[b][position / page_size].
+
+    k, v [tokens, heads, head_dim] fp16 or bf16; table int32 [sequences, width], cu int32
+    [sequences + 1], start int32 [sequences].  A position must be written by one token only.
+    """
+    desc = _cache(cache)
+    if k.dtype not in _16BIT:
+        raise ValueError("k must be fp16 or bf16")
+    for t, what in ((k, "k"), (v, "v")):
+        _heads(t, k.dtype, what)
+    if k.shape != v.shape or k.shape[1] != desc.heads or k.shape[2] != desc.head_dim:
+        raise ValueError("k and v must be [tokens, heads, head_dim] with the cache's heads and head_dim")
+    count = start.numel()
+    _ints(start, (count,), "start")
+    _ints(cu, (count + 1,), "cu")
+    _table(table, count)
+    _status_ok(status)
+    with _launching(stream, cache.k_codes, cache.k_params, cache.v_codes, cache.v_params, k, v, table, cu, start,
+                    status) as s:
+        _check(lib().gptq_kv4_append(ctypes.byref(desc), _ptr(k), *_strides(k), _ptr(v), *_strides(v),
+                                     _DTYPE_CODE[k.dtype], k.shape[0], _ptr(table), table.shape[1], _ptr(cu),
+                                     _ptr(start), count, _ptr(status), s), "gptq_kv4_append")
+    return cache
+
+
+def kv4_read(cache: KV4Cache, table: torch.Tensor, cu: torch.Tensor, tokens: int, start: Optional[torch.Tensor] = None,
+             dtype=torch.bfloat16, status: Optional[torch.Tensor] = None,
+             stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(k, v) [tokens, heads, head_dim] as the cache holds them: row t, cu[b] <= t < cu[b + 1], is
+    position start[b] + t - cu[b] of sequence b (start None: 0).  Rows of no sequence are not written."""
+    desc = _cache(cache)
+    if dtype not in _DTYPE_CODE:
+        raise ValueError("dtype must be float32, float16 or bfloat16")
+    count = cu.numel() - 1
+    if count < 0 or tokens < 0:
+        raise ValueError("cu must be int32 [sequences + 1] and tokens not negative")
+    _ints(cu, (count + 1,), "cu")
+    if start is not None:
+        _ints(start, (count,), "start")
+    _table(table, count)
+    _status_ok(status)
+    with _launching(stream, cache.k_codes, cache.k_params, cache.v_codes, cache.v_params, table, cu, start,
+                    status) as s:
+        k = torch.empty((int(tokens), desc.heads, desc.head_dim), dtype=dtype, device=cache.k_codes.device)
+        v = torch.empty_like(k)
+        _check(lib().gptq_kv4_read(ctypes.byref(desc), _ptr(table), table.shape[1], _ptr(cu), _ptr(start), count,
+                                   int(tokens), _DTYPE_CODE[dtype], _ptr(k), _ptr(v), _ptr(status), s),
+               "gptq_kv4_read")
+    return k, v
+
+
+def kv4_attention_workspace_size(count: int, heads_q: int, heads_kv: int, head_dim: int, width: int,
+                                 page_size: int) -> int:
+    return int(lib().gptq_kv4_attention_workspace_size(count, heads_q, heads_kv, head_dim, width, page_size))
+
+
+def kv4_attention(q: torch.Tensor, cache: KV4Cache, table: torch.Tensor, lengths: torch.Tensor,
+                  scale: Optional[float] = None, ws: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """o [sequences, heads_q, head_dim]: one query token per sequence against positions
+    0 .. lengths[b] - 1 of its cache (lengths int32 [sequences]; 0 gives a row of 0)."""
+    desc = _cache(cache)
+    if q.dtype not in _16BIT:
+        raise ValueError("q must be fp16 or bf16")
+    _heads(q, q.dtype, "q")
+    count, hq, d = q.shape
+    if d != desc.head_dim or hq % desc.heads != 0:
+        raise ValueError("q must have the cache's head size and a multiple of its heads")
+    _ints(lengths, (count,), "lengths")
+    _table(table, count)
+    _status_ok(status)
+    with _launching(stream, cache.k_codes, cache.k_params, cache.v_codes, cache.v_params, q, table, lengths, ws, out,
+                    status) as s:
+        need = kv4_attention_workspace_size(count, hq, desc.heads, d, table.shape[1], desc.page_size)
+        if ws is None or ws.numel() * ws.element_size() < need:
+            ws = workspace(need, q.device)
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        _heads(out, q.dtype, "out")
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        _apart(out, q)
+        _check(lib().gptq_kv4_attention(ctypes.byref(desc), _ptr(q), *_strides(q), _DTYPE_CODE[q.dtype], count, hq,
+                                        _ptr(table), table.shape[1], _ptr(lengths),
+                                        float(d ** -0.5 if scale is None else scale), _ptr(out), *_strides(out),
+                                        _ptr(ws), ws.numel() * ws.element_size(), _ptr(status), s),
+               "gptq_kv4_attention")
+    return out

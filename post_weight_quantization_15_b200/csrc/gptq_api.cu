@@ -25,6 +25,30 @@ cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
 bool valid_bits(int bits) { return bits == 2 || bits == 3 || bits == 4 || bits == 8; }
 bool valid_gs(int gs) { return gs == -1 || gs == 32 || gs == 64 || gs == 128; }
+bool valid_dtype(int t) { return t == GPTQ_F32 || t == GPTQ_F16 || t == GPTQ_BF16; }
+bool valid_dtype16(int t) { return t == GPTQ_F16 || t == GPTQ_BF16; }
+
+// A [tokens, heads, head_dim] operand of 16-bit values read or written in 16-byte pieces.
+bool valid_heads(const void* p, int64_t token_stride, int64_t head_stride) {
+  return p != nullptr && aligned(p, 16) && token_stride >= 0 && head_stride >= 0 && token_stride % 8 == 0 &&
+         head_stride % 8 == 0;
+}
+
+int check_cache(const gptq_kv4_cache* c, KV4Cache* out) {
+  if (c == nullptr || c->k_codes == nullptr || c->k_params == nullptr || c->v_codes == nullptr ||
+      c->v_params == nullptr || c->pages < 1 || c->heads < 1)
+    return GPTQ_ERR_INVALID_ARG;
+  if (!aligned(c->k_codes, 16) || !aligned(c->k_params, 16) || !aligned(c->v_codes, 16) || !aligned(c->v_params, 16))
+    return GPTQ_ERR_INVALID_ARG;
+  if (c->head_dim != 64 && c->head_dim != 128) return GPTQ_ERR_UNSUPPORTED;
+  if ((c->group != 32 && c->group != 64 && c->group != 128) || c->group > c->head_dim) return GPTQ_ERR_UNSUPPORTED;
+  if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)) != 0)
+    return GPTQ_ERR_UNSUPPORTED;
+  if (c->heads > 65535) return GPTQ_ERR_UNSUPPORTED;
+  *out = KV4Cache{{c->k_codes, c->v_codes}, {c->k_params, c->v_params}, c->pages, c->page_size, c->heads,
+                  c->head_dim, c->group};
+  return GPTQ_OK;
+}
 
 }  // namespace
 
@@ -276,6 +300,120 @@ int gptq_residual_add(const void* X, const float* Y, int64_t count, void* Xn, in
   if (!aligned(X, 8) || !aligned(Y, 16) || !aligned(Xn, 8)) return GPTQ_ERR_INVALID_ARG;
   if (count == 0) return GPTQ_OK;
   return launch_residual_add(X, Y, count, Xn, d_status, as_stream(stream));
+}
+
+int gptq_add_norm(const void* X, int x_dtype, int64_t ld_x, const void* Y, int y_dtype, int64_t ld_y,
+                  const void* weight, const void* bias, const void* post_weight, const void* post_bias,
+                  const void* gate, int64_t ld_gate, int p_dtype, int tokens, int d, float alpha, float eps, int center,
+                  void* Xn, int64_t ld_xn, void* h, int64_t ld_h, int32_t* d_status, void* stream) {
+  if (tokens < 0 || d < 1 || !valid_dtype(x_dtype) || !valid_dtype(p_dtype) || !(eps >= 0.f))
+    return GPTQ_ERR_INVALID_ARG;
+  if (tokens == 0) return GPTQ_OK;
+  if (X == nullptr || weight == nullptr || h == nullptr || ld_x < d || ld_h < d) return GPTQ_ERR_INVALID_ARG;
+  if (Y != nullptr && (!valid_dtype(y_dtype) || ld_y < d || Xn == nullptr || ld_xn < d)) return GPTQ_ERR_INVALID_ARG;
+  if (Y == nullptr && (post_weight != nullptr || gate != nullptr)) return GPTQ_ERR_INVALID_ARG;
+  if (post_bias != nullptr && post_weight == nullptr) return GPTQ_ERR_INVALID_ARG;
+  if (gate != nullptr && ld_gate != 0 && ld_gate < d) return GPTQ_ERR_INVALID_ARG;
+  if (d > 32768) return GPTQ_ERR_UNSUPPORTED;
+  return launch_add_norm(X, x_dtype, ld_x, Y, y_dtype, ld_y, weight, bias, post_weight, post_bias, gate, ld_gate,
+                         p_dtype, tokens, d, alpha, eps, center, Xn, ld_xn, h, ld_h, d_status, as_stream(stream));
+}
+
+int gptq_rope_qkv(const void* X, int x_dtype, int64_t ld, const float* bias, const float* cos, const float* sin,
+                  int max_pos, int rot, int interleaved, const int32_t* positions, int tokens, int heads_q,
+                  int heads_kv, int head_dim, int out_dtype, void* q, void* k, void* v, int32_t* d_status,
+                  void* stream) {
+  if (tokens < 0 || heads_q < 1 || heads_kv < 1 || head_dim < 2 ||
+      head_dim % 2 != 0 || rot < 0 || rot % 2 != 0 || rot > head_dim)
+    return GPTQ_ERR_INVALID_ARG;
+  if (!valid_dtype(x_dtype) || !valid_dtype16(out_dtype)) return GPTQ_ERR_INVALID_ARG;
+  if (tokens == 0) return GPTQ_OK;
+  if (X == nullptr || q == nullptr || k == nullptr || v == nullptr) return GPTQ_ERR_INVALID_ARG;
+  if (rot > 0 && (cos == nullptr || sin == nullptr || max_pos < 1)) return GPTQ_ERR_INVALID_ARG;
+  const int64_t cols = ((int64_t)heads_q + 2 * (int64_t)heads_kv) * head_dim;
+  if (cols > (1 << 30)) return GPTQ_ERR_UNSUPPORTED;
+  if (ld < cols) return GPTQ_ERR_INVALID_ARG;
+  return launch_rope_qkv(X, x_dtype, ld, bias, cos, sin, max_pos, rot, interleaved, positions, tokens, heads_q,
+                         heads_kv, head_dim, out_dtype, q, k, v, d_status, as_stream(stream));
+}
+
+int gptq_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                   int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                   int64_t v_head_stride, int dtype, const int32_t* cu_q, const int32_t* cu_k, int count, int total_q,
+                   int total_k, int heads_q, int heads_kv, int head_dim, float scale, int causal, void* o,
+                   int64_t o_token_stride, int64_t o_head_stride, int32_t* d_status, void* stream) {
+  if (count < 0 || total_q < 0 || total_k < 0 || heads_q < 1 || heads_kv < 1 || heads_q % heads_kv != 0)
+    return GPTQ_ERR_INVALID_ARG;
+  if (!valid_dtype16(dtype) || head_dim < 1 || !(scale == scale)) return GPTQ_ERR_INVALID_ARG;
+  if (head_dim % 8 != 0 || head_dim > 128 || heads_q > 65535) return GPTQ_ERR_UNSUPPORTED;
+  if (count == 0 || total_q == 0) return GPTQ_OK;
+  if (cu_q == nullptr || cu_k == nullptr || !valid_heads(q, q_token_stride, q_head_stride) ||
+      !valid_heads(o, o_token_stride, o_head_stride))
+    return GPTQ_ERR_INVALID_ARG;
+  if (total_k > 0 && (!valid_heads(k, k_token_stride, k_head_stride) || !valid_heads(v, v_token_stride, v_head_stride)))
+    return GPTQ_ERR_INVALID_ARG;
+  const AttentionArgs A{q, k, v, o, q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride,
+                        v_head_stride, o_token_stride, o_head_stride, cu_q, cu_k, count, total_q, total_k, heads_q,
+                        heads_kv, head_dim, scale, causal};
+  return launch_attention(A, dtype, d_status, as_stream(stream));
+}
+
+int gptq_kv4_append(const gptq_kv4_cache* cache, const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                    const void* v, int64_t v_token_stride, int64_t v_head_stride, int dtype, int tokens,
+                    const int32_t* table, int width, const int32_t* cu, const int32_t* start, int count,
+                    int32_t* d_status, void* stream) {
+  KV4Cache C;
+  const int rc = check_cache(cache, &C);
+  if (rc != GPTQ_OK) return rc;
+  if (tokens < 0 || count < 0 || width < 0 || !valid_dtype16(dtype)) return GPTQ_ERR_INVALID_ARG;
+  if (tokens == 0 || count == 0) return GPTQ_OK;
+  if (table == nullptr || width < 1 || cu == nullptr || start == nullptr ||
+      !valid_heads(k, k_token_stride, k_head_stride) || !valid_heads(v, v_token_stride, v_head_stride))
+    return GPTQ_ERR_INVALID_ARG;
+  return launch_kv4_append(C, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, dtype, tokens,
+                           table, width, cu, start, count, d_status, as_stream(stream));
+}
+
+int gptq_kv4_read(const gptq_kv4_cache* cache, const int32_t* table, int width, const int32_t* cu,
+                  const int32_t* start, int count, int tokens, int dtype, void* k, void* v, int32_t* d_status,
+                  void* stream) {
+  KV4Cache C;
+  const int rc = check_cache(cache, &C);
+  if (rc != GPTQ_OK) return rc;
+  if (tokens < 0 || count < 0 || width < 0 || !valid_dtype(dtype)) return GPTQ_ERR_INVALID_ARG;
+  if (tokens == 0 || count == 0) return GPTQ_OK;
+  if (table == nullptr || width < 1 || cu == nullptr || k == nullptr || v == nullptr || !aligned(k, 16) ||
+      !aligned(v, 16))
+    return GPTQ_ERR_INVALID_ARG;
+  return launch_kv4_read(C, table, width, cu, start, count, tokens, dtype, k, v, d_status, as_stream(stream));
+}
+
+size_t gptq_kv4_attention_workspace_size(int count, int heads_q, int heads_kv, int head_dim, int width,
+                                         int page_size) {
+  if (count < 1 || heads_q < 1 || heads_kv < 1 || head_dim < 1 || width < 1 || page_size < 1) return 0;
+  return kv4_attention_ws_bytes(count, heads_q, heads_kv, head_dim, (int64_t)width * page_size);
+}
+
+int gptq_kv4_attention(const gptq_kv4_cache* cache, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                       int dtype, int count, int heads_q, const int32_t* table, int width, const int32_t* lengths,
+                       float scale, void* o, int64_t o_token_stride, int64_t o_head_stride, void* ws,
+                       size_t ws_bytes, int32_t* d_status, void* stream) {
+  KV4Cache C;
+  const int rc = check_cache(cache, &C);
+  if (rc != GPTQ_OK) return rc;
+  if (count < 0 || width < 0 || heads_q < 1 || heads_q % C.heads != 0 || !valid_dtype16(dtype) || !(scale == scale))
+    return GPTQ_ERR_INVALID_ARG;
+  if (heads_q > 65535 || count > 65535) return GPTQ_ERR_UNSUPPORTED;
+  if (count == 0) return GPTQ_OK;
+  if (table == nullptr || width < 1 || lengths == nullptr || !valid_heads(q, q_token_stride, q_head_stride) ||
+      !valid_heads(o, o_token_stride, o_head_stride))
+    return GPTQ_ERR_INVALID_ARG;
+  if ((int64_t)width * C.page_size > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
+  if (ws == nullptr || !aligned(ws, 256) ||
+      ws_bytes < kv4_attention_ws_bytes(count, heads_q, C.heads, C.head_dim, (int64_t)width * C.page_size))
+    return GPTQ_ERR_WORKSPACE;
+  return launch_kv4_attention(C, q, q_token_stride, q_head_stride, dtype, count, heads_q, table, width, lengths,
+                              scale, o, o_token_stride, o_head_stride, ws, d_status, as_stream(stream));
 }
 
 int gptq_pack(const uint8_t* codes, int out, int n, int bits, int32_t* qweight, void* stream) {

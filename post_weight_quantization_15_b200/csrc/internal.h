@@ -122,6 +122,45 @@ int launch_transpose_bf16(const void* X, int rows, int cols, int64_t ldx, void* 
 int launch_silu_mul(const float* G, const float* U, int64_t count, void* h, const int32_t* st, cudaStream_t s);
 int launch_residual_add(const void* X, const float* Y, int64_t count, void* Xn, const int32_t* st, cudaStream_t s);
 
+// ---- a decoder block's attention half (norm.cu, rope.cu, attention.cu, kv4*.cu) ----
+int launch_add_norm(const void* X, int x_dtype, int64_t ld_x, const void* Y, int y_dtype, int64_t ld_y,
+                    const void* weight, const void* bias, const void* post_weight, const void* post_bias,
+                    const void* gate, int64_t ld_gate, int p_dtype, int tokens, int d, float alpha, float eps,
+                    int center, void* Xn, int64_t ld_xn, void* h, int64_t ld_h, const int32_t* st, cudaStream_t s);
+int launch_rope_qkv(const void* X, int x_dtype, int64_t ld, const float* bias, const float* cos, const float* sin,
+                    int max_pos, int rot, int interleaved, const int32_t* positions, int tokens, int hq, int hk,
+                    int d, int out_dtype, void* q, void* k, void* v, int32_t* st, cudaStream_t s);
+// Packed sequences: sequence b's queries are rows cu_q[b] .. cu_q[b + 1] - 1 of q and o, its
+// keys and values rows cu_k[b] .. cu_k[b + 1] - 1 of k and v.  Strides in elements.
+struct AttentionArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;
+  int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs;   // token and head strides
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int count, total_q, total_k, heads_q, heads_kv, head_dim;
+  float scale;
+  int causal;
+};
+int launch_attention(const AttentionArgs& A, int dtype, int32_t* st, cudaStream_t s);
+// The 4-bit cache: [0] keys, [1] values (layout in kv4.cuh).
+struct KV4Cache {
+  int32_t* codes[2];
+  uint16_t* params[2];
+  int pages, page_size, heads, head_dim, group;
+};
+int launch_kv4_append(const KV4Cache& C, const void* k, int64_t k_ts, int64_t k_hs, const void* v, int64_t v_ts,
+                      int64_t v_hs, int dtype, int tokens, const int32_t* table, int width, const int32_t* cu,
+                      const int32_t* start, int count, int32_t* st, cudaStream_t s);
+int launch_kv4_read(const KV4Cache& C, const int32_t* table, int width, const int32_t* cu, const int32_t* start,
+                    int count, int tokens, int dtype, void* k, void* v, int32_t* st, cudaStream_t s);
+size_t kv4_attention_ws_bytes(int count, int heads_q, int heads_kv, int head_dim, int64_t max_len);
+int launch_kv4_attention(const KV4Cache& C, const void* q, int64_t q_ts, int64_t q_hs, int dtype, int count,
+                         int heads_q, const int32_t* table, int width, const int32_t* lengths, float scale, void* o,
+                         int64_t o_ts, int64_t o_hs, void* ws, int32_t* st, cudaStream_t s);
+
 // ---- tensor-core GEMM: C -= A . B^T in 3 x TF32 (operands pre-split) ---------
 // store = false: C -= A.B^T; store = true: C = A.B^T (C may be null then, if Chi/Clo are given).
 // Chi/Clo (optional, leading dimension ldh) receive the TF32 split of the result.

@@ -1,0 +1,155 @@
+// The rotary split of a q/k/v product (gptq_rope_qkv): the fp32 rows a product of the
+// stacked q, k and v layers gives, plus their bias, become q, k and v in 16 bits; q and k
+// features (a, b) of a pair turn by their token's angle,
+//
+//   a' = a cos - b sin        b' = a sin + b cos,
+//
+// pairs being (i, i + rot/2) of a head, or (2i, 2i + 1) when interleaved; features from
+// rot on and all of v pass through.  The tables hold the cosines and sines per position.
+//
+// Bound: HBM (4 bytes in, 2 out per value).  One pass, W pairs per thread: 16 values read
+// as 16-byte pieces and written as two of them (W = 8); W = 4 where rot or the head size
+// asks for it, W = 1 for any even rot and any alignment.  A block stays within one token,
+// whose table rows its heads share in L1.
+#include "common.cuh"
+#include "internal.h"
+#include "vec_io.cuh"
+
+namespace gptq {
+
+namespace {
+
+struct RopeArgs {
+  const void* X;
+  int64_t ld;
+  const float* bias;
+  const float* cos;
+  const float* sin;
+  const int32_t* positions;
+  int max_pos, rot, interleaved;
+  int tokens, hq, hk, d;
+  void* q;
+  void* k;
+  void* v;
+};
+
+template <int W, typename T>
+__device__ __forceinline__ void loadw(const T* p, float (&v)[W]) {
+  if constexpr (W == 8) load8(p, v);
+  else if constexpr (W == 4) load4(p, v);
+  else v[0] = load_as_float(p);
+}
+template <int W, typename T>
+__device__ __forceinline__ void storew(T* p, const float (&v)[W]) {
+  if constexpr (W == 8) store8(p, v);
+  else if constexpr (W == 4) store4(p, v);
+  else store_from_float(p, v[0]);
+}
+
+// Thread: 2 W values of one head of one token; a head has d / (2 W) such units (W = 1:
+// rot and d even), the first rot / (2 W) of them rotated in q and k heads.
+template <typename TX, typename TO, int W>
+__global__ void __launch_bounds__(256) rope_qkv_kernel(const RopeArgs A, int units, int32_t* st) {
+  if (has_error(st)) return;
+  const int t = (int)blockIdx.x;
+  const int heads = A.hq + 2 * A.hk;
+  int pos = A.positions != nullptr ? A.positions[t] : t;
+  if (A.rot > 0 && (pos < 0 || pos >= A.max_pos)) {
+    if (threadIdx.x == 0 && blockIdx.y == 0) set_error(st, GPTQ_ERR_INVALID_ARG, t, STAGE_ROPE);
+    pos = 0;
+  }
+  const TX* row = static_cast<const TX*>(A.X) + (int64_t)t * A.ld;
+  for (int u = (int)blockIdx.y * 256 + (int)threadIdx.x; u < heads * units; u += 256 * (int)gridDim.y) {
+    const int head = u / units, j = u % units;
+    const bool turn = head < A.hq + A.hk && j * 2 * W < A.rot;
+    // the unit's two runs of W values inside the head
+    const bool split = turn && !A.interleaved;
+    const int i0 = split ? j * W : j * 2 * W;
+    const int i1 = split ? j * W + A.rot / 2 : j * 2 * W + W;
+    const int c0 = head * A.d + i0, c1 = head * A.d + i1;
+    float a[W], b[W];
+    loadw<W>(row + c0, a);
+    loadw<W>(row + c1, b);
+    if (A.bias != nullptr) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        a[i] += A.bias[c0 + i];
+        b[i] += A.bias[c1 + i];
+      }
+    }
+    if (turn) {
+      const float* cs = A.cos + (int64_t)pos * (A.rot / 2) + j * W;
+      const float* sn = A.sin + (int64_t)pos * (A.rot / 2) + j * W;
+      float c[W], s[W];
+      loadw<W>(cs, c);
+      loadw<W>(sn, s);
+      if (A.interleaved) {
+        // pair i of the unit: values 2i and 2i + 1 of the 2 W consecutive ones
+        float x[2 * W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) { x[i] = a[i]; x[W + i] = b[i]; }
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          const float lo = x[2 * i], hi = x[2 * i + 1];
+          x[2 * i] = lo * c[i] - hi * s[i];
+          x[2 * i + 1] = lo * s[i] + hi * c[i];
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) { a[i] = x[i]; b[i] = x[W + i]; }
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          const float lo = a[i], hi = b[i];
+          a[i] = lo * c[i] - hi * s[i];
+          b[i] = lo * s[i] + hi * c[i];
+        }
+      }
+    }
+    TO* dst;
+    if (head < A.hq) dst = static_cast<TO*>(A.q) + ((int64_t)t * A.hq + head) * A.d;
+    else if (head < A.hq + A.hk) dst = static_cast<TO*>(A.k) + ((int64_t)t * A.hk + head - A.hq) * A.d;
+    else dst = static_cast<TO*>(A.v) + ((int64_t)t * A.hk + head - A.hq - A.hk) * A.d;
+    storew<W>(dst + i0, a);
+    storew<W>(dst + i1, b);
+  }
+}
+
+template <typename TX, typename TO>
+void launch(const RopeArgs& A, int w, int32_t* st, cudaStream_t s) {
+  const int units = A.d / (2 * w);
+  const int64_t all = (int64_t)(A.hq + 2 * A.hk) * units;
+  const dim3 grd((unsigned)A.tokens, (unsigned)(cdiv(all, 256) < 64 ? cdiv(all, 256) : 64));
+  if (w == 8) rope_qkv_kernel<TX, TO, 8><<<grd, 256, 0, s>>>(A, units, st);
+  else if (w == 4) rope_qkv_kernel<TX, TO, 4><<<grd, 256, 0, s>>>(A, units, st);
+  else rope_qkv_kernel<TX, TO, 1><<<grd, 256, 0, s>>>(A, units, st);
+}
+
+template <typename TX>
+void launch_out(const RopeArgs& A, int w, int out_dtype, int32_t* st, cudaStream_t s) {
+  if (out_dtype == GPTQ_F16) launch<TX, __half>(A, w, st, s);
+  else launch<TX, __nv_bfloat16>(A, w, st, s);
+}
+
+bool al16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+}  // namespace
+
+int launch_rope_qkv(const void* X, int x_dtype, int64_t ld, const float* bias, const float* cos, const float* sin,
+                    int max_pos, int rot, int interleaved, const int32_t* positions, int tokens, int hq, int hk,
+                    int d, int out_dtype, void* q, void* k, void* v, int32_t* st, cudaStream_t s) {
+  RopeArgs A{X, ld, bias, cos, sin, positions, max_pos, rot, interleaved, tokens, hq, hk, d, q, k, v};
+  const int xb = x_dtype == GPTQ_F32 ? 4 : 2;
+  const bool al = al16(X) && (ld * xb) % 16 == 0 && al16(q) && al16(k) && al16(v) && (rot == 0 || (al16(cos) && al16(sin)));
+  int w = 1;
+  if (al && rot % 16 == 0 && d % 16 == 0) w = 8;
+  else if (al && rot % 8 == 0 && d % 8 == 0) w = 4;
+  const double cols = (double)(hq + 2 * hk) * d;
+  TraceScope ts("rope_qkv", "byte", tokens * (cols * (xb + 2) + 4.0 * rot), s);
+  if (x_dtype == GPTQ_F32) launch_out<float>(A, w, out_dtype, st, s);
+  else if (x_dtype == GPTQ_F16) launch_out<__half>(A, w, out_dtype, st, s);
+  else launch_out<__nv_bfloat16>(A, w, out_dtype, st, s);
+  GPTQ_LAUNCH_CHECK();
+  return GPTQ_OK;
+}
+
+}  // namespace gptq

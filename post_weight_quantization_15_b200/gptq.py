@@ -55,6 +55,12 @@ class _TraceEvent(ctypes.Structure):
                 ("end_ms", ctypes.c_double)]
 
 
+class _KV4(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_params", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_params", ctypes.c_void_p), ("pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("group", ctypes.c_int)]
+
+
 class GptqError(RuntimeError):
     def __init__(self, code: int, where: str, info: Optional[int] = None):
         self.code = code
@@ -141,6 +147,22 @@ def lib() -> ctypes.CDLL:
     L.gptq_silu_mul.argtypes = [P, P, I64, P, P, P]
     L.gptq_residual_add.restype = I
     L.gptq_residual_add.argtypes = [P, P, I64, P, P, P]
+    D = ctypes.POINTER(_KV4)
+    L.gptq_add_norm.restype = I
+    L.gptq_add_norm.argtypes = [P, I, I64, P, I, I64, P, P, P, P, P, I64, I, I, I, F, F, I, P, I64, P, I64, P, P]
+    L.gptq_rope_qkv.restype = I
+    L.gptq_rope_qkv.argtypes = [P, I, I64, P, P, P, I, I, I, P, I, I, I, I, I, P, P, P, P, P]
+    L.gptq_attention.restype = I
+    L.gptq_attention.argtypes = [P, I64, I64, P, I64, I64, P, I64, I64, I, P, P, I, I, I, I, I, I, F, I, P, I64, I64,
+                                 P, P]
+    L.gptq_kv4_append.restype = I
+    L.gptq_kv4_append.argtypes = [D, P, I64, I64, P, I64, I64, I, I, P, I, P, P, I, P, P]
+    L.gptq_kv4_read.restype = I
+    L.gptq_kv4_read.argtypes = [D, P, I, P, P, I, I, I, P, P, P, P]
+    L.gptq_kv4_attention_workspace_size.restype = SZ
+    L.gptq_kv4_attention_workspace_size.argtypes = [I, I, I, I, I, I]
+    L.gptq_kv4_attention.restype = I
+    L.gptq_kv4_attention.argtypes = [D, P, I64, I64, I, I, I, P, I, P, F, P, I64, I64, P, SZ, P, P]
     L.gptq_probe_fp32_peak.restype = I
     L.gptq_probe_fp32_peak.argtypes = [P, I, I, P]
     L.gptq_quantize_layer_noalloc.restype = I
