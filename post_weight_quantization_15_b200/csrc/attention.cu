@@ -4,53 +4,250 @@
 // sees no key gives 0; a key that a query does not see takes no part in it, whatever its
 // row holds.
 //
-// One warp per query and head: 32 keys at a time, a lane per key for the scores, a running
-// maximum and sum in fp32, then the lanes over the features for the values.
+// One pass over the keys with a running maximum m and sum l per query (scores s):
+//   m' = max(m, max_j s_j),  p_j = 2^(c (s_j - m')),  l' = l f + sum_j p_j,
+//   o' = o f + sum_j p_j v_j,  f = 2^(c (m - m')),  c = scale log2(e),  and o / l at the end.
+// While m' exceeds m by less than 2^8 in the weights, m is kept (f = 1): the weights stay
+// below 256 and the accumulated o needs no rescaling, which then is rare.
+//
+// A block takes 256 queries of one head as two tiles of 128, and the keys and values in
+// tiles of 128, on the tcgen05 tensor cores with the accumulators in TMEM:
+//   warps 0-3, 4-7   one tile each, a thread per query: S from TMEM, the softmax in
+//                    registers, P back over S as 16-bit values, and at the end O / l;
+//   warp 8           TMA loads of Q (once) and a ring of K and V tiles;
+//   warp 9           one thread issues the products: S = Q K^T (both from shared memory),
+//                    O += P V (P from TMEM, V from shared memory with its features
+//                    contiguous).  While one tile is in its softmax, the other's products run.
+// Every wait is bounded (GPTQ_ERR_TIMEOUT).
+//
+// Rows that no query may see: scores of keys past a row's limit are replaced before they are
+// used; values past the sequence's end are zeroed in shared memory.  Inside a sequence a
+// causal tile still multiplies weights of 0 with values behind the diagonal, which is
+// exact unless one of them is not finite: a query whose result holds a NaN is therefore
+// computed again one key at a time (seen_row), reading only what it sees.
 #include <math.h>
+
+#include <climits>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
-#include "kv4.cuh"
+#include "tc_common.cuh"
 #include "vec_io.cuh"
 
 namespace gptq {
 
 namespace {
 
-template <typename T>
-__global__ void __launch_bounds__(128) attention_rows_kernel(const AttentionArgs A, int32_t* st) {
-  __shared__ float qs[4][128];
-  if (has_error(st)) return;
-  const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
-  const int t = (int)blockIdx.x * 4 + warp, h = (int)blockIdx.y;
-  if (t >= A.total_q) return;
-  const int b = packed_sequence(A.cu_q, A.count, t);
-  if (b < 0) return;
-  const int q0 = A.cu_q[b], q1 = A.cu_q[b + 1], k0 = A.cu_k[b], k1 = A.cu_k[b + 1];
-  if (q0 < 0 || q1 > A.total_q || k0 < 0 || k1 < k0 || k1 > A.total_k) {
-    if (lane == 0) set_error(st, GPTQ_ERR_INVALID_ARG, b, STAGE_ATTENTION);
-    return;
+constexpr int TQ = 128;                   // queries of a tile, keys of a tile
+constexpr int ATHREADS = 320;
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float KEEP = 8.f;               // log2 of the largest weight under a kept maximum
+
+template <int KD>
+struct AttnSmem {
+  static constexpr int kTile = TQ * KD * 2;
+  static constexpr int kStages = KD == 128 ? 5 : 10;
+  uint8_t q[2][kTile];
+  uint8_t kv[kStages][kTile];
+  uint64_t q_full[2];
+  uint64_t kv_full[kStages];
+  uint64_t kv_empty[kStages];
+  uint64_t s_full[2];
+  uint64_t p_full[2];
+  uint64_t o_full[2];
+  uint64_t v_clean;
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  int skip;
+  int seq, tile;                          // this block's sequence and pair of tiles (-1: none)
+};
+
+// One tile's place: its queries, what they see, and how many key tiles that takes.
+struct Tile {
+  int row0, rows;                         // first query (of the sequence) and how many are real
+  int shift;                              // query i sees keys below min(lk, i + shift)
+  int blocks;
+};
+
+__device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// 32 columns of this thread's TMEM lane; the values are there after tmem_wait(v).
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+      : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+        "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+        "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+        "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+      :: "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+      :: "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+         "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]),
+         "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]),
+         "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+      :: "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+         "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] . B[smem], kind::f16: A as 16-bit pairs per column, a row per lane.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                           bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+
+// B operand with its N dimension contiguous (values: a token's features), 128-byte
+// swizzle: rows of 64 features, 8-token atoms of 1024 bytes, the next 64 features
+// `lead` bytes on.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t addr, uint32_t lead) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lead >> 4) & 0x3FFFu) << 16;  // leading byte offset: the next 64 features
+  d |= (uint64_t)(1024u >> 4) << 32;             // stride byte offset: 8 tokens
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+      ::"r"(tc::smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+__device__ __forceinline__ bool drain_wait(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = tc::globaltimer();
+  while (!tc::mbar_try_wait(bar, parity)) {
+    if (tc::globaltimer() - t0 > 1000000000ull) return false;
   }
+  return true;
+}
+
+// A whole warp waits for a barrier's phase (lane 0 polls).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  int ok = 0;
+  if ((threadIdx.x & 31) == 0) ok = tc::mbar_wait(bar, parity, abort_flag);
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// The sequence and the pair of tiles of slot `slot` (sequences in order, a sequence's
+// pairs from the last, which sees the most keys, to the first); whole warp.  Sequences with
+// bad bounds have no pairs and are recorded.
+__device__ __forceinline__ void find_work(const AttentionArgs& A, int slot, int32_t* st, int& seq, int& tile) {
+  const int lane = threadIdx.x & 31;
+  seq = -1;
+  tile = 0;
+  int base = 0;
+  for (int b0 = 0; b0 < A.count; b0 += 32) {
+    const int b = b0 + lane;
+    int pairs = 0;
+    if (b < A.count) {
+      const int q0 = A.cu_q[b], q1 = A.cu_q[b + 1], k0 = A.cu_k[b], k1 = A.cu_k[b + 1];
+      if (q0 < 0 || q1 < q0 || q1 > A.total_q || k0 < 0 || k1 < k0 || k1 > A.total_k)
+        set_error(st, GPTQ_ERR_INVALID_ARG, b, STAGE_ATTENTION);
+      else
+        pairs = (int)(((int64_t)(q1 - q0) + 2 * TQ - 1) / (2 * TQ));
+    }
+    int incl = pairs;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, base + incl > slot);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      seq = b0 + src;
+      tile = __shfl_sync(0xffffffffu, base + incl - 1 - slot, src);
+      return;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+__device__ __forceinline__ Tile make_tile(const AttentionArgs& A, int first, int lq, int lk) {
+  Tile t;
+  t.row0 = first;
+  t.rows = max(0, min(TQ, lq - first));
+  t.shift = A.causal ? 1 + lk - lq : lk;
+  const int last = t.rows > 0 ? (A.causal ? min(lk, first + t.rows - 1 + t.shift) : lk) : 0;
+  t.blocks = last > 0 ? (last + TQ - 1) / TQ : 0;
+  return t;
+}
+
+// One query against the keys it sees, one after another, by a whole warp (see above).
+template <typename T>
+__device__ __noinline__ void seen_row(const AttentionArgs& A, int t, int h, int hk, int k0, int seen) {
+  const int lane = threadIdx.x & 31;
   const T* q = static_cast<const T*>(A.q) + t * A.q_ts + h * A.q_hs;
-  const int hk = h / (A.heads_q / A.heads_kv);
-  for (int i = lane; i < A.head_dim; i += 32) qs[warp][i] = load_as_float(q + i) * A.scale;
-  __syncwarp();
-  int seen = k1 - k0;
-  if (A.causal) seen = min(seen, t - q0 + 1 + (k1 - k0) - (q1 - q0));
   float m = -INFINITY, l = 0.f;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   for (int j0 = 0; j0 < seen; j0 += 32) {
     const int j = j0 + lane;
     float sc = -INFINITY;
     if (j < seen) {
-      const T* k = static_cast<const T*>(A.k) + (k0 + j) * A.k_ts + hk * A.k_hs;
+      const T* k = static_cast<const T*>(A.k) + (int64_t)(k0 + j) * A.k_ts + hk * A.k_hs;
       sc = 0.f;
       for (int i = 0; i < A.head_dim; i += 8) {
-        float x[8];
+        float x[8], y[8];
         load8(k + i, x);
+        load8(q + i, y);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sc = fmaf(qs[warp][i + e], x[e], sc);
+        for (int e = 0; e < 8; ++e) sc = fmaf(y[e], x[e], sc);
       }
+      sc *= A.scale;
     }
     float mn = sc;
     for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
@@ -65,7 +262,7 @@ __global__ void __launch_bounds__(128) attention_rows_kernel(const AttentionArgs
     for (int o = 0; o < 32 && j0 + o < seen; ++o) {
       const float w = __shfl_sync(0xffffffffu, p, o);
       l += w;
-      const T* v = static_cast<const T*>(A.v) + (k0 + j0 + o) * A.v_ts + hk * A.v_hs;
+      const T* v = static_cast<const T*>(A.v) + (int64_t)(k0 + j0 + o) * A.v_ts + hk * A.v_hs;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (e * 32 + lane < A.head_dim) acc[e] = fmaf(w, load_as_float(v + e * 32 + lane), acc[e]);
@@ -77,15 +274,327 @@ __global__ void __launch_bounds__(128) attention_rows_kernel(const AttentionArgs
     if (e * 32 + lane < A.head_dim) store_from_float(o + e * 32 + lane, seen > 0 ? acc[e] / l : 0.f);
 }
 
+template <int KD, typename T>
+__global__ void __launch_bounds__(ATHREADS, 1)
+attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                 const __grid_constant__ CUtensorMap tv, const __grid_constant__ AttentionArgs A, int32_t* st) {
+  using Smem = AttnSmem<KD>;
+  constexpr int NST = Smem::kStages, TILE = Smem::kTile;
+  constexpr uint32_t FMT = std::is_same<T, __half>::value ? 0 : 1;
+  constexpr uint32_t IDESC_S = tc::idesc_f32acc(FMT, TQ, TQ);
+  constexpr uint32_t IDESC_O = tc::idesc_f32acc(FMT, TQ, KD) | (1u << 16);    // B with N contiguous
+  constexpr uint32_t O_COL = 2 * TQ;                                          // TMEM: S0, S1, O0, O1
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Smem& S = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = (int)blockIdx.x % A.heads_q, hk = h / (A.heads_q / A.heads_kv);
+
+  if (warp == 9) tc::tmem_alloc<512>(&S.tmem_base);
+  if (warp == 0) {
+    int seq, tile;
+    find_work(A, (int)blockIdx.x / A.heads_q, h == 0 ? st : nullptr, seq, tile);
+    if (lane == 0) {
+      S.seq = seq;
+      S.tile = tile;
+      S.skip = seq < 0 || has_error(st);
+      S.abort = 0;
+      for (int i = 0; i < 2; ++i) {
+        tc::mbar_init(&S.q_full[i], 1);
+        tc::mbar_init(&S.s_full[i], 1);
+        tc::mbar_init(&S.p_full[i], 4);
+        tc::mbar_init(&S.o_full[i], 1);
+      }
+      for (int i = 0; i < NST; ++i) { tc::mbar_init(&S.kv_full[i], 1); tc::mbar_init(&S.kv_empty[i], 1); }
+      tc::mbar_init(&S.v_clean, 32);
+      tc::mbar_init(&S.drain, 1);
+      tc::fence_barrier_init();
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t taddr = S.tmem_base;
+  volatile int* abort_flag = &S.abort;
+  int armed[NST];
+#pragma unroll
+  for (int i = 0; i < NST; ++i) armed[i] = 0;
+  bool q_armed[2] = {false, false};
+  bool mma_committed = false;
+
+  if (!S.skip) {
+    const int q0 = A.cu_q[S.seq], k0 = A.cu_k[S.seq];
+    const int lq = A.cu_q[S.seq + 1] - q0, lk = A.cu_k[S.seq + 1] - k0;
+    const Tile tl[2] = {make_tile(A, S.tile * 2 * TQ, lq, lk), make_tile(A, S.tile * 2 * TQ + TQ, lq, lk)};
+    const int blocks = max(tl[0].blocks, tl[1].blocks);
+    // the last tile of values reaches past the sequence's end: its rows there are zeroed
+    const int tail = blocks * TQ > lk ? lk - (blocks - 1) * TQ : 0;
+
+    if (warp == 8) {
+      if (lane == 0) {
+        for (int it = 0; it < 2 * blocks; ++it) {
+          if (it < 2 && tl[it].blocks > 0) {
+            tc::mbar_arrive_expect_tx(&S.q_full[it], TILE);
+#pragma unroll
+            for (int c = 0; c < KD / 64; ++c)
+              tma_load_3d(S.q[it] + c * (TQ * 128), &tq, &S.q_full[it], c * 64, h, q0 + tl[it].row0);
+            q_armed[it] = true;
+          }
+          const int s = it % NST;
+          if (!tc::mbar_wait(&S.kv_empty[s], ((uint32_t)(it / NST) & 1u) ^ 1u, abort_flag)) break;
+          tc::mbar_arrive_expect_tx(&S.kv_full[s], TILE);
+          const CUtensorMap* map = (it & 1) ? &tv : &tk;
+#pragma unroll
+          for (int c = 0; c < KD / 64; ++c)
+            tma_load_3d(S.kv[s] + c * (TQ * 128), map, &S.kv_full[s], c * 64, hk, k0 + (it >> 1) * TQ);
+#pragma unroll
+          for (int i = 0; i < NST; ++i) armed[i] += i == s;
+        }
+      }
+      __syncwarp();
+      if (tail > 0) {
+        const int it = 2 * blocks - 1, s = it % NST;
+        if (warp_wait(&S.kv_full[s], (uint32_t)(it / NST) & 1u, abort_flag)) {
+          for (int i = tail * 8 + lane; i < TQ * 8; i += 32)
+#pragma unroll
+            for (int c = 0; c < KD / 64; ++c)
+              *reinterpret_cast<uint4*>(S.kv[s] + c * (TQ * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          tc::mbar_arrive(&S.v_clean);
+        }
+      }
+    } else if (warp == 9) {
+      if (lane == 0) {
+        // S of tile t from the key tile in stage s
+        auto product_s = [&](int t, int s) {
+          const uint32_t a0 = tc::smem_u32(S.q[t]), b0 = tc::smem_u32(S.kv[s]);
+#pragma unroll
+          for (int k = 0; k < KD / 16; ++k) {
+            const uint32_t off = (k / 4) * (TQ * 128) + (k % 4) * 32;
+            tc::mma_f16(taddr + t * TQ, tc::sdesc_k_sw128(a0 + off), tc::sdesc_k_sw128(b0 + off), IDESC_S, k > 0);
+          }
+          tc::mma_commit(&S.s_full[t]);
+        };
+        bool ok = blocks > 0;
+        if (ok) ok = tc::mbar_wait(&S.kv_full[0], 0, abort_flag);
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (tl[t].blocks == 0) continue;
+          ok = tc::mbar_wait(&S.q_full[t], 0, abort_flag);
+          if (!ok) break;
+          tc::tc_fence_after();
+          product_s(t, 0);
+        }
+        if (ok) tc::mma_commit(&S.kv_empty[0]);
+        for (int j = 0; j < blocks && ok; ++j) {
+          const int iv = 2 * j + 1, ik = 2 * j + 2;
+          const int sv = iv % NST, sk = ik % NST;
+          ok = tc::mbar_wait(&S.kv_full[sv], (uint32_t)(iv / NST) & 1u, abort_flag);
+          if (ok && tail > 0 && j == blocks - 1) ok = tc::mbar_wait(&S.v_clean, 0, abort_flag);
+          if (ok && j + 1 < blocks) ok = tc::mbar_wait(&S.kv_full[sk], (uint32_t)(ik / NST) & 1u, abort_flag);
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (j < tl[t].blocks) {
+              ok = tc::mbar_wait(&S.p_full[t], (uint32_t)j & 1u, abort_flag);
+              if (!ok) break;
+              tc::tc_fence_after();
+              const uint32_t b0 = tc::smem_u32(S.kv[sv]);
+#pragma unroll
+              for (int k = 0; k < TQ / 16; ++k)
+                mma_f16_ts(taddr + O_COL + t * KD, taddr + t * TQ + k * 8, sdesc_mn_sw128(b0 + k * 2048, TQ * 128),
+                           IDESC_O, j > 0 || k > 0);
+              if (j + 1 == tl[t].blocks) tc::mma_commit(&S.o_full[t]);
+            }
+            if (t == 1) tc::mma_commit(&S.kv_empty[sv]);
+            if (j + 1 < tl[t].blocks) product_s(t, sk);
+            if (t == 1 && j + 1 < blocks) tc::mma_commit(&S.kv_empty[sk]);
+          }
+        }
+        // every commit has arrived before the block's shared memory is given up
+        tc::mma_commit(&S.drain);
+        mma_committed = true;
+        if (!*abort_flag) drain_wait(&S.drain, 0);
+      }
+    } else {
+      const int t = warp >> 2;                            // warps 0-3: tile 0, 4-7: tile 1
+      const Tile& me = tl[t];
+      const int r = (warp & 3) * 32 + lane;               // this thread's query in the tile
+      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t ts = taddr + lanes + t * TQ, to = taddr + lanes + O_COL + t * KD;
+      const int limit = r < me.rows ? max(0, min(lk, A.causal ? me.row0 + r + me.shift : lk)) : 0;
+      const float c0 = A.scale * LOG2E;
+      const float c = c0 > 0.f ? c0 : 1.f;
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int j = 0; j < me.blocks; ++j) {
+        ok = warp_wait(&S.s_full[t], (uint32_t)j & 1u, abort_flag);
+        if (!ok) break;
+        tc::tc_fence_after();
+        float s[TQ];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(ts + i * 32, s + i * 32);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_wait(s + i * 32);
+        if (!(c0 > 0.f)) {                                // a scale of 0 or below: the product first
+#pragma unroll
+          for (int i = 0; i < TQ; ++i) s[i] *= c0;
+        }
+        const int see = limit - j * TQ;
+        if (__any_sync(0xffffffffu, see < TQ)) {
+#pragma unroll
+          for (int i = 0; i < TQ; ++i) s[i] = i < see ? s[i] : -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int i = 4; i < TQ; i += 8) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mx[e] = fmaxf(mx[e], i + 4 + e < TQ ? fmaxf(s[i + e], s[i + 4 + e]) : s[i + e]);
+        }
+        const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+        if (j == 0) {
+          m = mn;
+        } else {
+          const bool up = (mn - m) * c > KEEP;            // -inf to finite included
+          if (__any_sync(0xffffffffu, up)) {
+            // S's arrival also says that the products into O issued before it are done
+            const float f = up ? exp2_approx((m - mn) * c) : 1.f;
+            if (up) m = mn;
+            l *= f;
+#pragma unroll 1
+            for (int i = 0; i < KD; i += 32) {
+              float o[32];
+              tmem_ld32(to + i, o);
+              tmem_wait(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= f;
+              tmem_st32(to + i, o);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : m * c;
+        const uint64_t c2 = pack_f32x2(c, c), r2 = pack_f32x2(-ref, -ref);
+        uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < TQ; i += 32) {
+          uint32_t p[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float a, b;
+            unpack_f32x2(fma2(pack_f32x2(s[i + 2 * e], s[i + 2 * e + 1]), c2, r2), a, b);
+            a = exp2_approx(a);
+            b = exp2_approx(b);
+            sum[e & 3] = add2(sum[e & 3], pack_f32x2(a, b));
+            p[e] = pack2(a, b, T());
+          }
+          tmem_st16(ts + i / 2, p);
+        }
+        float a, b;
+        unpack_f32x2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
+        l += a + b;
+        tmem_st_wait();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&S.p_full[t]);
+      }
+      if (ok && me.rows > 0) {
+        if (me.blocks > 0) ok = warp_wait(&S.o_full[t], 0, abort_flag);
+        if (ok) {
+          tc::tc_fence_after();
+          const bool mine = r < me.rows;
+          T* dst = static_cast<T*>(A.o) + (int64_t)(q0 + me.row0 + r) * A.o_ts + h * A.o_hs;
+          const float inv = 1.f / l;
+          bool nan = false;
+#pragma unroll 1
+          for (int i = 0; i < KD; i += 32) {
+            float o[32];
+            if (me.blocks > 0) {
+              tmem_ld32(to + i, o);
+              tmem_wait(o);
+            }
+            if (limit == 0) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = 0.f;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                o[e] *= inv;
+                nan |= o[e] != o[e];
+              }
+            }
+            if (mine) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8)
+                if (i + e < A.head_dim) store8(dst + i + e, o + e);
+            }
+          }
+          unsigned again = __ballot_sync(0xffffffffu, nan && mine);
+          while (again != 0) {
+            const int src = __ffs(again) - 1;
+            again &= again - 1;
+            seen_row<T>(A, q0 + me.row0 + (warp & 3) * 32 + src, h, hk, k0, __shfl_sync(0xffffffffu, limit, src));
+          }
+        }
+      }
+    }
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {
+    if (warp == 8 && lane == 0) {
+#pragma unroll
+      for (int i = 0; i < NST; ++i)
+        if (armed[i] > 0) drain_wait(&S.kv_full[i], (uint32_t)(armed[i] - 1) & 1u);
+      for (int i = 0; i < 2; ++i)
+        if (q_armed[i]) drain_wait(&S.q_full[i], 0);
+    }
+    if (warp == 9 && lane == 0 && mma_committed) drain_wait(&S.drain, 0);
+    if (threadIdx.x == 0) set_error(st, GPTQ_ERR_TIMEOUT, blockIdx.x, STAGE_ATTENTION);
+    __syncthreads();
+  }
+  if (warp == 9) {
+    __syncwarp();
+    tc::tmem_dealloc<512>(taddr);
+  }
+}
+
+template <int KD, typename T>
+int launch(const AttentionArgs& A, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, int32_t* st,
+           cudaStream_t s) {
+  const size_t smem = sizeof(AttnSmem<KD>) + 1024;
+  auto* kernel = attention_kernel<KD, T>;
+  GPTQ_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  // at most total_q / 256 + count pairs of tiles, and one slot that reads every bound
+  const int64_t slots = A.total_q / (2 * TQ) + (int64_t)A.count + 1;
+  if (slots * A.heads_q > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
+  kernel<<<(unsigned)(slots * A.heads_q), ATHREADS, smem, s>>>(tq, tk, tv, A, st);
+  GPTQ_LAUNCH_CHECK();
+  return GPTQ_OK;
+}
+
+// [tokens, heads, head_dim] in boxes of 128 tokens by 64 features; features past head_dim
+// and tokens past the end read as 0.
+int head_map(CUtensorMap* map, CUtensorMapDataType dt, const void* p, int tokens, int heads, int head_dim, int64_t ts,
+             int64_t hs) {
+  return make_tmap_3d(map, dt, p, (uint64_t)head_dim, (uint64_t)heads, (uint64_t)tokens, (uint64_t)hs * 2,
+                      (uint64_t)ts * 2, 64, 1, TQ, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 }  // namespace
 
 int launch_attention(const AttentionArgs& A, int dtype, int32_t* st, cudaStream_t s) {
+  CUtensorMap tq, tk, tv;
+  const CUtensorMapDataType dt = dtype == GPTQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  int rc = head_map(&tq, dt, A.q, A.total_q, A.heads_q, A.head_dim, A.q_ts, A.q_hs);
+  if (rc != GPTQ_OK) return rc;
+  tk = tv = tq;                           // without any key nothing is loaded through them
+  if (A.total_k > 0) {
+    rc = head_map(&tk, dt, A.k, A.total_k, A.heads_kv, A.head_dim, A.k_ts, A.k_hs);
+    if (rc == GPTQ_OK) rc = head_map(&tv, dt, A.v, A.total_k, A.heads_kv, A.head_dim, A.v_ts, A.v_hs);
+    if (rc != GPTQ_OK) return rc;
+  }
   TraceScope ts("attention", "", 0.0, s);
-  const dim3 grd((unsigned)cdiv(A.total_q, 4), (unsigned)A.heads_q);
-  if (dtype == GPTQ_F16) attention_rows_kernel<__half><<<grd, 128, 0, s>>>(A, st);
-  else attention_rows_kernel<__nv_bfloat16><<<grd, 128, 0, s>>>(A, st);
-  GPTQ_LAUNCH_CHECK();
-  return GPTQ_OK;
+  if (A.head_dim <= 64)
+    return dtype == GPTQ_F16 ? launch<64, __half>(A, tq, tk, tv, st, s) : launch<64, __nv_bfloat16>(A, tq, tk, tv, st, s);
+  return dtype == GPTQ_F16 ? launch<128, __half>(A, tq, tk, tv, st, s) : launch<128, __nv_bfloat16>(A, tq, tk, tv, st, s);
 }
 
 }  // namespace gptq

@@ -284,4 +284,9 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr) {
 int make_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner, uint64_t outer,
                  uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle);
 
+// The same with three dimensions (the strides of the second and third in bytes).
+int make_tmap_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner, uint64_t mid,
+                 uint64_t outer, uint64_t mid_stride_bytes, uint64_t outer_stride_bytes, uint32_t box_inner,
+                 uint32_t box_mid, uint32_t box_outer, CUtensorMapSwizzle swizzle);
+
 }  // namespace gptq

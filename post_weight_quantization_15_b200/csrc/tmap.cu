@@ -42,4 +42,22 @@ int make_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, 
   return r == CUDA_SUCCESS ? GPTQ_OK : GPTQ_ERR_INVALID_ARG;
 }
 
+int make_tmap_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner, uint64_t mid,
+                 uint64_t outer, uint64_t mid_stride_bytes, uint64_t outer_stride_bytes, uint32_t box_inner,
+                 uint32_t box_mid, uint32_t box_outer, CUtensorMapSwizzle swizzle) {
+  std::call_once(g_once, resolve);
+  if (g_encode == nullptr) return GPTQ_ERR_CUDA;
+  if (inner == 0 || mid == 0 || outer == 0 || (mid_stride_bytes % 16) != 0 || (outer_stride_bytes % 16) != 0 ||
+      (reinterpret_cast<uintptr_t>(base) % 16) != 0)
+    return GPTQ_ERR_INVALID_ARG;
+  cuuint64_t dims[3] = {inner, mid, outer};
+  cuuint64_t strides[2] = {mid_stride_bytes, outer_stride_bytes};
+  cuuint32_t box[3] = {box_inner, box_mid, box_outer};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = g_encode(map, dtype, 3, const_cast<void*>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? GPTQ_OK : GPTQ_ERR_INVALID_ARG;
+}
+
 }  // namespace gptq
