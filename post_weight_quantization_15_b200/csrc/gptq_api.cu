@@ -390,7 +390,8 @@ int gptq_kv4_read(const gptq_kv4_cache* cache, const int32_t* table, int width, 
 
 size_t gptq_kv4_attention_workspace_size(int count, int heads_q, int heads_kv, int head_dim, int width,
                                          int page_size) {
-  if (count < 1 || heads_q < 1 || heads_kv < 1 || head_dim < 1 || width < 1 || page_size < 1) return 0;
+  if (count < 1 || heads_q < 1 || heads_kv < 1 || heads_q % heads_kv != 0 || head_dim < 1 || width < 1 || page_size < 1)
+    return 0;
   return kv4_attention_ws_bytes(count, heads_q, heads_kv, head_dim, (int64_t)width * page_size);
 }
 
@@ -409,6 +410,7 @@ int gptq_kv4_attention(const gptq_kv4_cache* cache, const void* q, int64_t q_tok
       !valid_heads(o, o_token_stride, o_head_stride))
     return GPTQ_ERR_INVALID_ARG;
   if ((int64_t)width * C.page_size > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
+  if ((int64_t)C.pages * C.heads * C.page_size > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;   // TMA rows
   if (ws == nullptr || !aligned(ws, 256) ||
       ws_bytes < kv4_attention_ws_bytes(count, heads_q, C.heads, C.head_dim, (int64_t)width * C.page_size))
     return GPTQ_ERR_WORKSPACE;

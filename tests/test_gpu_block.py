@@ -11,6 +11,12 @@ Bounds (u = the output type's eps / 2, one rounding to nearest; w = 2^-24):
             and below, plus 2^-21 + |s - max| 2w for the exponential and its argument; rounded to
             16 bits for the product with v (up); the normaliser has the same relative errors bar up.
   values    sums over n keys: (n + 16) 2w of sum p|v|.
+  small weights in fp16: the largest weight of a row is at least 1 (the kept maximum is never above
+            the row's), so the sum of weights is too.  In attention a weight below 2^-14 is off by up to
+            2^-25: n 2^-25 max|v| in all.  In the 4-bit cache a weight times its scale s is held as
+            p s 2^(10 - e), 2^e <= the group's largest scale S: off by up to 2^-25 of that unit,
+            2^(e - 35) <= 2^-35 S, times |c - z| <= 15.  A group with scale S spans 15 S, so one of its
+            values is at least 7 S: 15 S <= 2.2 max|v|, and n tokens give less than n 2^-33 max|v|.
 """
 import numpy as np
 import pytest
@@ -201,8 +207,11 @@ def test_rope_qkv_records_a_position_outside_the_tables():
 # --------------------------------------------------------------------------- #
 # attention
 # --------------------------------------------------------------------------- #
-def _attn_tol(q, k, v, cu_q, cu_k, scale, causal, dtype, up, dq=0.0):
-    """(oracle, bound): dq = what q's own rounding inside the kernel adds to a score, per sum|k|."""
+def _attn_tol(q, k, v, cu_q, cu_k, scale, causal, dtype, up, dq=0.0, small=None):
+    """(oracle, bound): dq = what q's own rounding inside the kernel adds to a score, per sum|k|;
+    small = what a weight below its 16-bit type's normal range is off by, per max|v|."""
+    if small is None:
+        small = 2.0 ** -25 if dtype == HF else 0.0
     hq, hk, d = q.shape[1], k.shape[1], q.shape[2]
     ref, mag = B.attention(q, k, v, cu_q, cu_k, scale, causal)
     tol = np.zeros(q.shape)
@@ -218,7 +227,8 @@ def _attn_tol(q, k, v, cu_q, cu_k, scale, causal, dtype, up, dq=0.0):
             s = abs(scale) * (qa @ ka.T).max(1)                  # the largest sum of |terms|
             ds = s * (d + 16) * 2 * W + abs(scale) * dq * qa.max(1) * ka.sum(1).max()
             rel = 2 * (ds + 2.0 ** -21 + 2 * s * 2 * W) + up + (n + 16) * 2 * W
-            tol[qs, h] = rel[:, None] * mag[qs, h]
+            vmax = np.nan_to_num(np.abs(v[ks, g]), nan=0.0, posinf=0.0).max()
+            tol[qs, h] = rel[:, None] * mag[qs, h] + small * n * vmax
     return ref, tol * (1 + U[dtype]) + U[dtype] * np.abs(np.nan_to_num(ref)) + TINY[dtype]
 
 
@@ -489,7 +499,7 @@ def test_kv4_attention(lens, hq, hk, d, group, page, dt):
     # inside the kernel q may be held in fp16 under a power of two: 2^-25 of its largest value;
     # the weights in fp16 (2^-11)
     ref, tol = _attn_tol(_np(q), k64, v64, list(range(len(lens) + 1)), _cu(lens), d ** -0.5, False, dt, 2.0 ** -11,
-                         dq=2.0 ** -25)
+                         dq=2.0 ** -25, small=2.0 ** -33)
     _close(o, ref, tol, "o")
     assert torch.equal(o, G.kv4_attention(q, cache, table, _int(lens)))
 
@@ -510,7 +520,7 @@ def test_kv4_attention_rows_behind_the_end_and_extremes():
         q[0, 0] = 0.0
         scale = 0.5 / mul if mul > 2.0 ** -100 else 1.0
         o = G.kv4_attention(q, cache, table, _int(lens), scale=scale)
-        ref, tol = _attn_tol(_np(q), k64, v64, [0, 1, 2], _cu(lens), scale, False, BF, 2.0 ** -11, dq=2.0 ** -25)
+        ref, tol = _attn_tol(_np(q), k64, v64, [0, 1, 2], _cu(lens), scale, False, BF, 2.0 ** -11, dq=2.0 ** -25, small=2.0 ** -33)
         _close(o, ref, tol, mul)
 
 
