@@ -410,7 +410,6 @@ int gptq_kv4_attention(const gptq_kv4_cache* cache, const void* q, int64_t q_tok
       !valid_heads(o, o_token_stride, o_head_stride))
     return GPTQ_ERR_INVALID_ARG;
   if ((int64_t)width * C.page_size > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
-  if ((int64_t)C.pages * C.heads * C.page_size > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;   // TMA rows
   if (ws == nullptr || !aligned(ws, 256) ||
       ws_bytes < kv4_attention_ws_bytes(count, heads_q, C.heads, C.head_dim, (int64_t)width * C.page_size))
     return GPTQ_ERR_WORKSPACE;

@@ -4,26 +4,32 @@
 // A sequence without tokens gives 0.
 //
 // Bound: HBM, the codes and their scales read once (and close behind it the issue slots
-// that unpack them).  The query heads of a k/v head are the rows of m16n8k16 products
-// (mma.sync, fp16 in, fp32 sums), up to 16 at a time.  Two codes are masked into the
-// mantissas of the fp16 pair 1024 + c (or 1024 + 16 c, from the next nibble) and one
-// packed subtraction (or fma) leaves c - z, an exact fp16 integer; scales stay outside:
-//   scores   q . k_t = sum over groups of s sum q (c - z), q held in fp16 under a power of
-//            two per row (its largest value in [2^11, 2^12): both 16-bit types fit, values
-//            below 2^-25 of the largest rounded);
-//   values   sum_t p_t s_t (c_t - z_t) with p_t s_t rounded to fp16 under a power of two
-//            per group (largest value below 2^15).
+// that unpack them).  Products are m16n8k16 (mma.sync, fp16 in, fp32 sums) with the query
+// heads of a k/v head, eight at a time, as columns and the cache as rows (tokens for the
+// scores, features for the values), so that no row is wasted on a group of eight or fewer:
+//   scores   K [16 tokens, D] . q^T [D, 8]; the weights, transposed in registers
+//            (movmatrix), are the B operand of  V^T [16 features, 16 tokens] . p^T.
+// Two codes are masked into the mantissas of the fp16 pair 1024 + c (or 1024 + 16 c, from
+// the next nibble) and one packed subtraction (or fma) leaves c - z, an exact fp16 integer;
+// scales stay outside:
+//   q . k_t = sum over groups of s sum q (c - z), q held in fp16 under a power of two per
+//            row (its largest value in [2^11, 2^12): both 16-bit types fit, values below
+//            2^-25 of the largest rounded);
+//   sum_t p_t s_t (c_t - z_t) with p_t s_t rounded to fp16 under a power of two per group
+//            (largest value below 2^15).
 // (Without the subtraction, c as an fp16 subnormal and z taken off the sums, the sums
 // cancel: the tensor cores align such products by their unnormalised exponents, and
 // results near 0 were off by 2^-17 of a scale.)
-// The running maximum is kept while it grows by less than 2^4 in the weights.
+// The running maximum is kept while no score passes it by more than 2^4 in the weights, so
+// lanes exchange maxima only when it moves.
 //
 // Work: the sequences' tiles of 32 tokens, all heads, in one line, cut into equal runs, one
-// per block of four warps (three blocks per SM); a block's warps take its tiles in turn,
-// each with a ring of its own that TMA fills (codes swizzled, scales as they lie).  A head
-// whose tiles fall to one block is finished there; otherwise the blocks leave their
-// (maximum, sum, weighted values) in the workspace and kv4_join_kernel, a dependent launch,
-// joins them in a fixed order.  Every wait is bounded (GPTQ_ERR_TIMEOUT).
+// per block of four warps; a block's warps take its tiles in turn, each with a ring of its
+// own that asynchronous 16-byte copies fill (the codes' pieces swizzled against bank
+// conflicts), so that the warps never wait for each other inside a head.  A head whose tiles
+// fall to one block is finished there; otherwise the blocks leave their (maximum, sum,
+// weighted values) in the workspace and kv4_join_kernel, a dependent launch, joins them in
+// a fixed order.
 #include <math.h>
 
 #include <climits>
@@ -31,18 +37,18 @@
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.cuh"
-#include "tc_common.cuh"
 #include "vec_io.cuh"
 
 namespace gptq {
 
 namespace {
 
-constexpr int BLOCKS = 148 * 3;           // resident blocks: the cut of the work, whatever the device
+constexpr int PER_SM = 4;
+constexpr int BLOCKS = 148 * PER_SM;      // resident blocks: the cut of the work, whatever the device
 constexpr int WARPS = 4;
 constexpr int TT = 32;                    // tokens of a tile
-constexpr int STAGES = 3;
-constexpr int ROWS = 16;                  // query heads of a product
+constexpr int STAGES = 2;
+constexpr int ROWS = 8;                   // query heads of a product
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float KEEP = 4.f;
 
@@ -55,7 +61,7 @@ struct KvaArgs {
   const int32_t* lengths;
   float* part_o;                          // [2 BLOCKS][rows][head_dim]
   float* part_ml;                         // [2 BLOCKS][rows][2]
-  int width, count, per, sets, rows;      // per: query heads of a k/v head, in sets of up to 16 (rows)
+  int width, count, per, sets, rows;      // per: query heads of a k/v head, in sets of up to 8 (rows)
   float scale;
   int half;                               // q and o are fp16 (else bf16)
 };
@@ -141,26 +147,36 @@ __device__ __forceinline__ int runs_of(int64_t all) {
 
 template <int D, int GROUP>
 struct KvaSmem {
-  static constexpr int kCodes = TT * D / 2;
-  static constexpr int kParams = TT * (D / GROUP) * 4;
   struct Stage {
-    alignas(512) uint8_t codes[2][kCodes];
-    uint8_t params[2][kParams];
+    uint8_t codes[2][TT * D / 2];         // keys, values: token rows, 16-byte pieces swizzled (piece())
+    __half2 params[2][TT * (D / GROUP)];
   };
   Stage ring[WARPS][STAGES];
+  int4 desc[WARPS][STAGES];               // sequence, head set | pages that exist << 28, first token, ord
   float out[ROWS][D];
   float ml[2][WARPS][ROWS][2];
-  int4 desc[WARPS][STAGES];
   int2 seg[2];
-  uint64_t full[WARPS][STAGES];
-  int abort, skip;
+  int skip;
 };
 
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// Where 16-byte piece `i` of token row `row` lies in a stage: a row has D / 32 pieces, and
+// rows that would share banks hold them in another order.
+template <int D>
+__device__ __forceinline__ uint32_t piece(int row, int i) {
+  return (uint32_t)(row * (D / 2) + ((i ^ (D == 128 ? (row >> 1) & 3 : (row >> 2) & 1)) << 4));
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 // Codes -> c - z: the nibbles at bits 0 and 16, or at bits 4 and 20, of x; zero.lo holds
@@ -182,22 +198,20 @@ __device__ __forceinline__ uint32_t code_hi(uint32_t x, const Zero& z) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
-}
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
 }
 
 // Eight consecutive q values; o values likewise.
@@ -211,24 +225,17 @@ __device__ __forceinline__ void store_o(const KvaArgs& A, int64_t off, const flo
 }
 
 template <int D, int GROUP>
-__global__ void __launch_bounds__(WARPS * 32, 3)
-kv4_attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-                     const __grid_constant__ KvaArgs A, int32_t* st) {
+__global__ void __launch_bounds__(WARPS * 32, PER_SM)
+kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
   using Smem = KvaSmem<D, GROUP>;
   constexpr int NG = D / GROUP;           // groups of a row
   constexpr int NW = D / 32;              // words of a key row per lane
-  constexpr int NT = TT / 8;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  Smem& S = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u));
+  constexpr int MT = D / 16;              // feature tiles of the values
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  Smem& S = *reinterpret_cast<Smem*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, j = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;");
-  if (threadIdx.x == 0) {
-    S.skip = has_error(st);
-    S.abort = 0;
-    for (int w = 0; w < WARPS; ++w)
-      for (int s = 0; s < STAGES; ++s) tc::mbar_init(&S.full[w][s], 1);
-    tc::fence_barrier_init();
-  }
+  if (threadIdx.x == 0) S.skip = has_error(st);
   const int heads = A.C.heads * A.sets;
   int64_t all = 0;
   {
@@ -250,80 +257,84 @@ kv4_attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
   const bool goes_on = __shfl_sync(0xffffffffu, ends.t + 1 < ends.tiles, 1) != 0;
   finder = Finder();
 
-  volatile int* abort_flag = &S.abort;
-  // this warp's tiles: begin + warp + 4 i
+  // this warp's tiles: begin + warp + 4 i; lane i holds what tile (made & ~31) + i needs
   const int mine = (int)((end - begin - warp + WARPS - 1) / WARPS);
-  const int box = min(A.C.page_size, TT), parts = TT / box;      // page rows of one copy; copies of a tile
-  const int page_shift = 31 - __clz(A.C.page_size);
+  const int box = min(A.C.page_size, TT), parts = TT / box;      // tokens of a tile in one page; pages of a tile
   int made = 0;
-  // the batch of 32 tiles that lane i describes tile (made & ~31) + i of
-  int row0 = 0, row1 = 0;
+  int64_t row0 = 0, row1 = 0;
   int4 d0 = make_int4(0, 0, 0, 0);
   auto produce = [&]() {
-    if (made >= mine) return;
-    if ((made & 31) == 0) {
-      const int i = made + lane;
-      const int64_t want = i < mine ? begin + warp + (int64_t)WARPS * i : -1;
-      const Place p = finder.find(A, heads, want);
-      if (want >= 0) {
-        const int head = p.hx / A.sets, t0 = p.t * TT;
-        int ok = 0;
+    if (made < mine) {
+      if ((made & 31) == 0) {
+        const int i = made + lane;
+        const int64_t want = i < mine ? begin + warp + (int64_t)WARPS * i : -1;
+        const Place p = finder.find(A, heads, want);
+        if (want >= 0) {
+          const int head = p.hx / A.sets, t0 = p.t * TT;
+          const int len = A.lengths[p.b];
+          int ok = 0;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          // a tile's second page may lie behind the sequence's end: its table entry is not read
-          const int pos = t0 + k * box;
-          int page = 0;
-          if (k < parts && pos < A.lengths[p.b]) {
-            page = kv4_page(A.C, A.table, A.width, p.b, pos);
-            if (page < 0) {
-              set_error(st, GPTQ_ERR_INVALID_ARG, p.b, STAGE_KV4_ATTENTION);
-              page = 0;
-            } else {
-              ok |= parts == 1 ? 3 : 1 << k;
+          for (int k = 0; k < 2; ++k) {
+            // rows of a second page behind the sequence's end are those of page 0, not used
+            const int pos = t0 + k * 16;
+            int page = 0;
+            if (pos < len) {
+              page = kv4_page(A.C, A.table, A.width, p.b, pos);
+              if (page < 0) {
+                set_error(st, GPTQ_ERR_INVALID_ARG, p.b, STAGE_KV4_ATTENTION);
+                page = 0;
+              } else {
+                ok |= 1 << k;
+              }
+            } else if (parts == 1) {
+              page = -1;                  // the same page as the first half
             }
+            const int64_t row = kv4_row(A.C, page, head, pos & (A.C.page_size - 1));
+            if (k == 0) row0 = row;
+            else row1 = page < 0 ? row0 + 16 : row;
           }
-          const int row = (int)kv4_row(A.C, page, head, pos & (A.C.page_size - 1));
-          if (k == 0) row0 = row;
-          else row1 = row;
+          d0 = make_int4(p.b, p.hx | (ok << 28), t0, (int)(p.ord - ord0));
         }
-        d0 = make_int4(p.b, p.hx | (ok << 28), t0, (int)(p.ord - ord0));
       }
-    }
-    const int src = made & 31, s = made % STAGES;
-    const int r0 = __shfl_sync(0xffffffffu, row0, src), r1 = __shfl_sync(0xffffffffu, row1, src);
-    const int4 d = make_int4(__shfl_sync(0xffffffffu, d0.x, src), __shfl_sync(0xffffffffu, d0.y, src),
-                             __shfl_sync(0xffffffffu, d0.z, src), __shfl_sync(0xffffffffu, d0.w, src));
-    if (lane == 0) {
-      S.desc[warp][s] = d;
+      const int src = made & 31, s = made % STAGES;
+      const int64_t r[2] = {__shfl_sync(0xffffffffu, row0, src), __shfl_sync(0xffffffffu, row1, src)};
+      if (lane == src) S.desc[warp][s] = d0;
       auto& stage = S.ring[warp][s];
-      uint64_t* bar = &S.full[warp][s];
-      tc::mbar_arrive_expect_tx(bar, 2 * (Smem::kCodes + Smem::kParams));
-      const uint32_t pb = (uint32_t)(box * NG * 4);
-      for (int k = 0; k < parts; ++k) {
-        const int r = k == 0 ? r0 : r1;
-        tc::tma_load_2d(stage.codes[0] + k * box * (D / 2), &tk, bar, 0, r);
-        tc::tma_load_2d(stage.codes[1] + k * box * (D / 2), &tv, bar, 0, r);
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-          bulk_load(tc::smem_u32(stage.params[n]) + k * pb, A.C.params[n] + (int64_t)r * NG * 2, pb,
-                    tc::smem_u32(bar));
+      for (int kv = 0; kv < 2; ++kv) {
+        constexpr int P16 = D / 2;        // pieces of 16 tokens
+        const uint32_t dst = smem_addr(stage.codes[kv]) + piece<D>(lane / (D / 32), lane % (D / 32));
+        const char* base = reinterpret_cast<const char*>(A.C.codes[kv]) + lane * 16;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int i = 0; i < P16 / 32; ++i)    // 32 pieces on, the rows' swizzle repeats
+            copy16(dst + (k * P16 + i * 32) * 16, base + r[k] * (D / 2) + i * 512);
+        constexpr int Q16 = 4 * NG;       // pieces of 16 tokens' scales and zero points
+        if (lane < 2 * Q16) {
+          const int k = lane / Q16;
+          copy16(smem_addr(stage.params[kv]) + lane * 16,
+                 reinterpret_cast<const char*>(A.C.params[kv]) + (k ? r[1] : r[0]) * (NG * 4) + (lane % Q16) * 16);
+        }
       }
+      ++made;
     }
-    __syncwarp();
-    ++made;
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
+#pragma unroll
   for (int i = 0; i < STAGES; ++i) produce();
+  __syncwarp();
 
-  // the state of the head set at hand: rows g and g + 8
-  float acc[D / 8][4], m[2], l[2];
+  // the state of the head set at hand: heads 2 j and 2 j + 1 of it
+  float acc[MT][4], m[2], l[2];
   int ve[NG];                             // weights of group i carry 2^(10 - ve[i])
-  uint32_t qa[D / 16][4];
-  float rf[2];
+  uint32_t qb[D / 16][2];                 // head g's query as operand
+  float rf[2] = {1.f, 1.f};               // log2 of a weight per unit of score
   int used = 0, cur = -1, at_b = 0, at_hx = 0;
 
   for (int ord = 0; ord <= ord1; ++ord) {
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
 #pragma unroll
@@ -336,6 +347,7 @@ kv4_attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
       const int4 d = S.desc[warp][s];
       if (d.w != ord) break;
       const int b = d.x, hx = d.y & 0x0fffffff, ok = (int)((uint32_t)d.y >> 28), t0 = d.z;
+      const int have = A.lengths[b] - t0;
       if (cur != ord) {
         // this warp's first tile of the head set: its queries as operands
         cur = ord;
@@ -343,236 +355,225 @@ kv4_attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
         at_hx = hx;
         const int head = hx / A.sets, first = head * A.per + (hx % A.sets) * ROWS;
         const int rows = min(ROWS, A.per - (hx % A.sets) * ROWS);
-        float x[2][NW][8];
-        float top[2] = {0.f, 0.f};
+        float x[NW][8];
+        float top = 0.f;
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int w = 0; w < NW; ++w) {
+          const int word = NG == 1 ? NW * j + w : j + 4 * w;
 #pragma unroll
-          for (int w = 0; w < NW; ++w) {
-            const int word = NG == 1 ? NW * j + w : j + 4 * w;
+          for (int e = 0; e < 8; ++e) x[w][e] = 0.f;
+          if (g < rows) load_q(A, (int64_t)b * A.q_ts + (int64_t)(first + g) * A.q_hs + word * 8, x[w]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[r][w][e] = 0.f;
-            if (g + 8 * r < rows)
-              load_q(A, (int64_t)b * A.q_ts + (int64_t)(first + g + 8 * r) * A.q_hs + word * 8, x[r][w]);
+          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[w][e]));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e2 = top > 0.f && top <= 3.4028235e38f ? ilogbf(top) : 0;
+        // a scale below 0 goes to the queries; one of 0 (or scores that vanish in fp32) makes them 0
+        float f = ldexpf(fabsf(A.scale) * LOG2E, e2 - 11);
+        const float sign = f == 0.f ? 0.f : (A.scale < 0.f ? -1.f : 1.f);
+        f = f == 0.f ? 1.f : f;
+        rf[0] = __shfl_sync(0xffffffffu, f, 8 * j);
+        rf[1] = __shfl_sync(0xffffffffu, f, 8 * j + 4);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) top[r] = fmaxf(top[r], fabsf(x[r][w][e]));
-          }
+        for (int w = 0; w < NW; ++w) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-          top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-          const int e2 = top[r] > 0.f && top[r] <= 3.4028235e38f ? ilogbf(top[r]) : 0;
-          rf[r] = ldexpf(A.scale * LOG2E, e2 - 11);
+          for (int e = 0; e < 8; ++e) x[w][e] = ldexpf(x[w][e], 11 - e2) * sign;
+          // a word's codes come in the pairs (i, i + 4)
 #pragma unroll
-          for (int w = 0; w < NW; ++w) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[r][w][e] = ldexpf(x[r][w][e], 11 - e2);
-            // a word's codes come in the pairs (i, i + 4)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              qa[2 * w + k][r] = pack2(x[r][w][2 * k], x[r][w][2 * k + 4], __half());
-              qa[2 * w + k][2 + r] = pack2(x[r][w][2 * k + 1], x[r][w][2 * k + 5], __half());
-            }
+          for (int k = 0; k < 2; ++k) {
+            qb[2 * w + k][0] = pack2(x[w][2 * k], x[w][2 * k + 4], __half());
+            qb[2 * w + k][1] = pack2(x[w][2 * k + 1], x[w][2 * k + 5], __half());
           }
         }
       }
-      const int have = A.lengths[b] - t0;
       const bool edge = have < TT || ok != 3;
-      int fine = 0;
-      if (lane == 0) fine = tc::mbar_wait(&S.full[warp][s], (uint32_t)(used / STAGES) & 1u, abort_flag);
-      fine = __shfl_sync(0xffffffffu, fine, 0);
-      if (fine) {
-        auto& stage = S.ring[warp][s];
-        const uint32_t kc = tc::smem_u32(stage.codes[0]), vc = tc::smem_u32(stage.codes[1]);
-        const __half2* kp = reinterpret_cast<const __half2*>(stage.params[0]);
-        const __half2* vp = reinterpret_cast<const __half2*>(stage.params[1]);
-        // token i of the tile counts
-        auto seen = [&](int i) { return i < have && ((ok >> (i >> 4)) & 1); };
+      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+      __syncwarp();
+      auto& stage = S.ring[warp][s];
+      const uint32_t kc = smem_addr(stage.codes[0]), vc = smem_addr(stage.codes[1]);
+      const __half2* kp = stage.params[0];
+      const __half2* vp = stage.params[1];
+      // token i of the tile counts
+      auto seen = [&](int i) { return i < have && ((ok >> (i >> 4)) & 1); };
 
-        // ---- scores ----
-        float sc[NT][4];
+      // ---- scores: tokens 16 h + g (+ 8) against heads 2 j, 2 j + 1 ----
+      float sc[2][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int row = n * 8 + g;
-          uint32_t w[NW];
-          if constexpr (NG == 1 && D == 128) {
-            const uint32_t a = kc + row * 64 + ((j ^ ((row >> 1) & 3)) << 4);
-            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
-          } else if constexpr (NG == 1) {
-            const uint32_t a = kc + row * 32 + (((j >> 1) ^ ((row >> 2) & 1)) << 4) + (j & 1) * 8;
-            asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
-          } else {
-            const uint32_t sw = D == 128 ? (row >> 1) & 3 : (row >> 2) & 1;
-#pragma unroll
-            for (int i = 0; i < NW; ++i) w[i] = lds32(kc + row * (D / 2) + ((i ^ sw) << 4) + j * 4);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
-#pragma unroll
-          for (int i = 0; i < NG; ++i) {
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
-            const Zero z = make_zero(__high2half2(kp[row * NG + i]));
-#pragma unroll
-            for (int k = i * NW / NG; k < (i + 1) * NW / NG; ++k) {
-              const uint32_t hi = w[k] >> 8;
-              mma16816(c, qa[2 * k], code_lo(w[k], z), code_hi(w[k], z));
-              mma16816(c, qa[2 * k + 1], code_lo(hi, z), code_hi(hi, z));
-            }
-            const float s0 = __low2float(kp[(n * 8 + 2 * j) * NG + i]);
-            const float s1 = __low2float(kp[(n * 8 + 2 * j + 1) * NG + i]);
-            sc[n][0] = fmaf(s0, c[0], sc[n][0]);
-            sc[n][1] = fmaf(s1, c[1], sc[n][1]);
-            sc[n][2] = fmaf(s0, c[2], sc[n][2]);
-            sc[n][3] = fmaf(s1, c[3], sc[n][3]);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[n][e] *= rf[e >> 1];
-          if (edge) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (!seen(n * 8 + 2 * j + (e & 1))) sc[n][e] = -INFINITY;
-          }
-        }
-
-        // ---- running maximum, weights and their sum ----
-        float mx[2];
-        bool up = false;
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[2][NW];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          mx[r] = m[r];
+          const int row = h * 16 + r * 8 + g;
+          if constexpr (NG == 1 && D == 128) {
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[r][0]), "=r"(w[r][1]), "=r"(w[r][2]), "=r"(w[r][3]) : "r"(kc + piece<D>(row, j)));
+          } else if constexpr (NG == 1) {
+            asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
+                         : "=r"(w[r][0]), "=r"(w[r][1]) : "r"(kc + piece<D>(row, j >> 1) + (j & 1) * 8));
+          } else {
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mx[r] = fmaxf(mx[r], fmaxf(sc[n][2 * r], sc[n][2 * r + 1]));
-          mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-          mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-          up |= mx[r] - m[r] > KEEP;
-        }
-        if (__any_sync(0xffffffffu, up)) {
-          float f[2];
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const bool mine_up = mx[r] - m[r] > KEEP;
-            f[r] = mine_up ? ex2(m[r] - mx[r]) : 1.f;
-            if (mine_up) m[r] = mx[r];
-            l[r] *= f[r];
+            for (int i = 0; i < NW; ++i) w[r][i] = lds32(kc + piece<D>(row, i) + j * 4);
           }
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][e] *= f[e >> 1];
         }
-        const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            sc[n][e] = ex2(sc[n][e] - ref[e >> 1]);
-            l[e >> 1] += sc[n][e];
-          }
-
-        // ---- values ----
-        uint32_t pa[NG][TT / 16][4];
-        __half2 zv[NG][NT];               // zero points of tokens 2 j, 2 j + 1
+        for (int e = 0; e < 4; ++e) sc[h][e] = 0.f;
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-          float sv[NT][2];
-          float top = 0.f;
+          const __half2 p0 = kp[(h * 16 + g) * NG + i], p1 = kp[(h * 16 + 8 + g) * NG + i];
+          const Zero z0 = make_zero(__high2half2(p0)), z1 = make_zero(__high2half2(p1));
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            {
-              __half2 p0 = vp[(n * 8 + 2 * j) * NG + i], p1 = vp[(n * 8 + 2 * j + 1) * NG + i];
-              if (edge) {
-                if (!seen(n * 8 + 2 * j)) p0 = __half2half2(__ushort_as_half((unsigned short)0));
-                if (!seen(n * 8 + 2 * j + 1)) p1 = __half2half2(__ushort_as_half((unsigned short)0));
-              }
-              sv[n][0] = __low2float(p0);
-              sv[n][1] = __low2float(p1);
-              zv[i][n] = __highs2half2(p0, p1);
-              top = fmaxf(top, fmaxf(fabsf(sv[n][0]), fabsf(sv[n][1])));
-            }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const int e2 = min((int)(__float_as_uint(top) >> 23) - 127, 15);   // top < 2^(e2 + 1)
-          if (e2 > ve[i]) {               // the same in every lane
-            const float f = ex2((float)(ve[i] - e2));
-            ve[i] = e2;
-            constexpr int PER = D / 8 / NG;
-#pragma unroll
-            for (int a = 0; a < PER; ++a)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[i * PER + a][e] *= f;
+          for (int k = i * NW / NG; k < (i + 1) * NW / NG; ++k) {
+            mma16816(c, code_lo(w[0][k], z0), code_lo(w[1][k], z1), code_hi(w[0][k], z0), code_hi(w[1][k], z1),
+                     qb[2 * k][0], qb[2 * k][1]);
+            const uint32_t x = w[0][k] >> 8, y = w[1][k] >> 8;
+            mma16816(c, code_lo(x, z0), code_lo(y, z1), code_hi(x, z0), code_hi(y, z1), qb[2 * k + 1][0],
+                     qb[2 * k + 1][1]);
           }
-          const float mul = __uint_as_float((uint32_t)(10 - ve[i] + 127) << 23);
-#pragma unroll
-          for (int k = 0; k < TT / 16; ++k) {
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const float s0 = sv[2 * k + n][0] * mul, s1 = sv[2 * k + n][1] * mul;
-              pa[i][k][2 * n] = pack2(sc[2 * k + n][0] * s0, sc[2 * k + n][1] * s1, __half());
-              pa[i][k][2 * n + 1] = pack2(sc[2 * k + n][2] * s0, sc[2 * k + n][3] * s1, __half());
-            }
-          }
+          const float s0 = __low2float(p0), s1 = __low2float(p1);
+          sc[h][0] = fmaf(s0, c[0], sc[h][0]);
+          sc[h][1] = fmaf(s0, c[1], sc[h][1]);
+          sc[h][2] = fmaf(s1, c[2], sc[h][2]);
+          sc[h][3] = fmaf(s1, c[3], sc[h][3]);
         }
-        auto vword = [&](int row, int word) {
-          const uint32_t sw = D == 128 ? (row >> 1) & 3 : (row >> 2) & 1;
-          return lds32(vc + row * (D / 2) + (((word >> 2) ^ sw) << 4) + (word & 3) * 4);
+        if (edge) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!seen(h * 16 + (e >> 1) * 8 + g)) sc[h][e] = -INFINITY;
+        }
+      }
+
+      // ---- the running maximum, weights and their sum ----
+      float mx[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        mx[r] = fmaxf(fmaxf(sc[0][r], sc[0][2 + r]), fmaxf(sc[1][r], sc[1][2 + r])) * rf[r];
+      if (__any_sync(0xffffffffu, mx[0] - m[0] > KEEP || mx[1] - m[1] > KEEP)) {
+        float f[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], o));
+          mx[r] = fmaxf(mx[r], m[r]);
+          f[r] = mx[r] == -INFINITY ? 1.f : ex2(m[r] - mx[r]);
+          m[r] = mx[r];
+          l[r] *= f[r];
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][e] *= f[e & 1];
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float ref = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = r; e < 4; e += 2) {
+            sc[h][e] = ex2(fmaf(sc[h][e], rf[r], -ref));
+            l[r] += sc[h][e];
+          }
+      }
+
+      // ---- values ----
+      uint32_t pb[NG][2][2];              // the weights of group i, tokens of half h, as B operand
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        float sv[2][2];
+        float top = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int t = h * 16 + r * 8 + g;
+            sv[h][r] = __low2float(vp[t * NG + i]);
+            if (edge && !seen(t)) sv[h][r] = 0.f;
+            top = fmaxf(top, fabsf(sv[h][r]));
+          }
+        int e2 = min((int)(__float_as_uint(top) >> 23) - 127, 15);     // top < 2^(e2 + 1)
+        if (__any_sync(0xffffffffu, e2 > ve[i])) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) e2 = max(e2, __shfl_xor_sync(0xffffffffu, e2, o));
+          const float f = ex2((float)(ve[i] - e2));
+          ve[i] = e2;
+#pragma unroll
+          for (int a = i * MT / NG; a < (i + 1) * MT / NG; ++a)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[a][e] *= f;
+        }
+        const float mul = __uint_as_float((uint32_t)(10 - ve[i] + 127) << 23);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float k = sv[h][r] * mul;
+            pb[i][h][r] = transpose8x8(pack2(sc[h][2 * r] * k, sc[h][2 * r + 1] * k, __half()));
+          }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int ta = h * 16 + 2 * j;    // this lane's tokens: ta, ta + 1, ta + 8, ta + 9
+        auto zeros = [&](int i, int t) {
+          __half2 p0 = vp[t * NG + i], p1 = vp[(t + 1) * NG + i];
+          const __half none = __ushort_as_half((unsigned short)0);
+          if (edge && !seen(t)) p0 = __half2half2(none);
+          if (edge && !seen(t + 1)) p1 = __half2half2(none);
+          return make_zero(__highs2half2(p0, p1));
         };
+        auto word = [&](int t, int w) { return lds32(vc + piece<D>(t, w >> 2) + (w & 3) * 4); };
+        if constexpr (GROUP >= 64) {
+          // rows g and g + 8 of feature tile (f, i): nibbles i and i + 4 of word 8 f + g
 #pragma unroll
-        for (int k = 0; k < TT / 16; ++k) {
-          const int ra = k * 16 + 2 * j;
-          if constexpr (GROUP >= 64) {
-            // column n of a product: word n (+ 8), nibble i of it per product
+          for (int f = 0; f < D / 64; ++f) {
+            const int w = 8 * f + g, grp = f * 64 / GROUP;
+            const Zero za = zeros(grp, ta), zb = zeros(grp, ta + 8);
+            const uint32_t wa = word(ta, w), wb = word(ta + 1, w), wc = word(ta + 8, w), wd = word(ta + 9, w);
+            uint32_t x0 = __byte_perm(wa, wb, 0x5410), x1 = __byte_perm(wa, wb, 0x7632);
+            uint32_t y0 = __byte_perm(wc, wd, 0x5410), y1 = __byte_perm(wc, wd, 0x7632);
+            const uint32_t p0 = pb[grp][h][0], p1 = pb[grp][h][1];
 #pragma unroll
-            for (int hf = 0; hf < D / 64; ++hf) {
-              const int word = g + 8 * hf;
-              const uint32_t wa = vword(ra, word), wb = vword(ra + 1, word);
-              const uint32_t wc = vword(ra + 8, word), wd = vword(ra + 9, word);
-              const uint32_t x[2] = {__byte_perm(wa, wb, 0x5410), __byte_perm(wa, wb, 0x7632)};
-              const uint32_t y[2] = {__byte_perm(wc, wd, 0x5410), __byte_perm(wc, wd, 0x7632)};
-              const Zero za = make_zero(zv[hf * 64 / GROUP][2 * k]), zb = make_zero(zv[hf * 64 / GROUP][2 * k + 1]);
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const uint32_t x8 = x[u] >> 8, y8 = y[u] >> 8;
-                const int a = hf * 8 + u * 4;
-                const uint32_t(&p)[4] = pa[hf * 64 / GROUP][k];
-                mma16816(acc[a], p, code_lo(x[u], za), code_lo(y[u], zb));
-                mma16816(acc[a + 1], p, code_hi(x[u], za), code_hi(y[u], zb));
-                mma16816(acc[a + 2], p, code_lo(x8, za), code_lo(y8, zb));
-                mma16816(acc[a + 3], p, code_hi(x8, za), code_hi(y8, zb));
-              }
+            for (int i = 0; i < 4; i += 2) {
+              mma16816(acc[4 * f + i], code_lo(x0, za), code_lo(x1, za), code_lo(y0, zb), code_lo(y1, zb), p0, p1);
+              mma16816(acc[4 * f + i + 1], code_hi(x0, za), code_hi(x1, za), code_hi(y0, zb), code_hi(y1, zb), p0, p1);
+              x0 >>= 8; x1 >>= 8; y0 >>= 8; y1 >>= 8;
             }
-          } else {
-            // a product's columns stay in one group of 32: word n mod 4 of it, nibble 2 i + n / 4
+          }
+        } else {
+          // a tile's rows stay in one group of 32: nibbles 2 i + g / 4 (and 4 on) of word g mod 4 of it
+          const int sh = (g >> 2) * 4;
 #pragma unroll
-            for (int i = 0; i < NG; ++i) {
-              const int word = 4 * i + (g & 3), sh = (g >> 2) * 4;
-              const uint32_t wa = vword(ra, word), wb = vword(ra + 1, word);
-              const uint32_t wc = vword(ra + 8, word), wd = vword(ra + 9, word);
-              const uint32_t x[2] = {__byte_perm(wa, wb, 0x5410) >> sh, __byte_perm(wa, wb, 0x7632) >> sh};
-              const uint32_t y[2] = {__byte_perm(wc, wd, 0x5410) >> sh, __byte_perm(wc, wd, 0x7632) >> sh};
-              const Zero za = make_zero(zv[i][2 * k]), zb = make_zero(zv[i][2 * k + 1]);
+          for (int q = 0; q < NG; ++q) {
+            const int w = 4 * q + (g & 3);
+            const Zero za = zeros(q, ta), zb = zeros(q, ta + 8);
+            const uint32_t wa = word(ta, w), wb = word(ta + 1, w), wc = word(ta + 8, w), wd = word(ta + 9, w);
+            uint32_t x0 = __byte_perm(wa, wb, 0x5410) >> sh, x1 = __byte_perm(wa, wb, 0x7632) >> sh;
+            uint32_t y0 = __byte_perm(wc, wd, 0x5410) >> sh, y1 = __byte_perm(wc, wd, 0x7632) >> sh;
 #pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                mma16816(acc[4 * i + 2 * u], pa[i][k], code_lo(x[u], za), code_lo(y[u], zb));
-                mma16816(acc[4 * i + 2 * u + 1], pa[i][k], code_lo(x[u] >> 8, za), code_lo(y[u] >> 8, zb));
-              }
+            for (int i = 0; i < 2; ++i) {
+              mma16816(acc[2 * q + i], code_lo(x0, za), code_lo(x1, za), code_lo(y0, zb), code_lo(y1, zb),
+                       pb[q][h][0], pb[q][h][1]);
+              x0 >>= 8; x1 >>= 8; y0 >>= 8; y1 >>= 8;
             }
           }
         }
       }
-      __syncwarp();
+      __syncwarp();                       // every lane has read the stage
       ++used;
       produce();
+      __syncwarp();                       // the next tiles' descriptors are there
     }
 
     // ---- the four warps' parts of this head set joined, in order ----
     float (*ml)[ROWS][2] = S.ml[ord & 1];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if (j == 0) {
-        ml[warp][g + 8 * r][0] = m[r];
-        ml[warp][g + 8 * r][1] = l[r];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+      if (g == 0) {
+        ml[warp][2 * j + r][0] = m[r];
+        ml[warp][2 * j + r][1] = l[r];
       }
     }
     if (cur == ord && lane == 0) S.seg[ord & 1] = make_int2(at_b, at_hx);
@@ -584,22 +585,22 @@ kv4_attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
     for (int r = 0; r < 2; ++r) {
       float top = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w][g + 8 * r][0]);
+      for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w][2 * j + r][0]);
       f[r] = m[r] == -INFINITY ? 0.f : ex2(m[r] - top);
     }
     for (int w = 0; w < WARPS; ++w) {
       if (warp == w) {
 #pragma unroll
-        for (int a = 0; a < D / 8; ++a) {
-          const int i = a * NG / (D / 8);
+        for (int a = 0; a < MT; ++a) {
+          const int i = a * NG / MT;
           const float mul = ve[i] < -116 ? 0.f : __uint_as_float((uint32_t)(ve[i] - 10 + 127) << 23);   // unset: acc is 0
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int col = 2 * j + (e & 1), row = g + 8 * (e >> 1);
-            const int dim = GROUP >= 64 ? 8 * (col + 8 * (a / 8)) + a % 8
-                                        : 8 * (4 * (a / 4) + (col & 3)) + 2 * (a % 4) + (col >> 2);
-            const float v = acc[a][e] * mul * f[e >> 1];
-            S.out[row][dim] = w == 0 ? v : S.out[row][dim] + v;
+            const int head = 2 * j + (e & 1), up = (e >> 1) * 4;
+            const int dim = GROUP >= 64 ? 8 * (8 * (a / 4) + g) + a % 4 + up
+                                        : 8 * (4 * (a / 2) + (g & 3)) + 2 * (a % 2) + (g >> 2) + up;
+            const float v = acc[a][e] * mul * f[e & 1];
+            S.out[head][dim] = w == 0 ? v : S.out[head][dim] + v;
           }
         }
       }
@@ -632,17 +633,6 @@ kv4_attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_consta
         }
       }
     }
-  }
-  if (*abort_flag) {
-    if (lane == 0) {
-      for (int s = 0; s < STAGES; ++s) {
-        const int n = (made - s + STAGES - 1) / STAGES;
-        const uint64_t t0 = tc::globaltimer();
-        while (n > 0 && !tc::mbar_try_wait(&S.full[warp][s], (uint32_t)(n - 1) & 1u))
-          if (tc::globaltimer() - t0 > 1000000000ull) break;
-      }
-    }
-    if (threadIdx.x == 0) set_error(st, GPTQ_ERR_TIMEOUT, (int)blockIdx.x, STAGE_KV4_ATTENTION);
   }
 }
 
@@ -733,19 +723,10 @@ int set_rows(int per) { return per < ROWS ? per : ROWS; }
 
 template <int D, int GROUP>
 int launch(const KvaArgs& A, int32_t* st, cudaStream_t s) {
-  // a cache row per line, in boxes of as many rows as a page or a tile holds
-  const uint64_t rows = (uint64_t)A.C.pages * A.C.heads * A.C.page_size;
-  const uint32_t box = (uint32_t)(A.C.page_size < TT ? A.C.page_size : TT);
-  const CUtensorMapSwizzle swz = D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
-  CUtensorMap map[2];
-  for (int i = 0; i < 2; ++i) {
-    const int rc = make_tmap_2d(&map[i], CU_TENSOR_MAP_DATA_TYPE_INT32, A.C.codes[i], D / 8, rows, D / 2, D / 8, box, swz);
-    if (rc != GPTQ_OK) return rc;
-  }
-  const size_t smem = sizeof(KvaSmem<D, GROUP>) + 1024;
+  const size_t smem = sizeof(KvaSmem<D, GROUP>);
   auto* kernel = kv4_attention_kernel<D, GROUP>;
   GPTQ_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  kernel<<<BLOCKS, WARPS * 32, smem, s>>>(map[0], map[1], A, st);
+  kernel<<<BLOCKS, WARPS * 32, smem, s>>>(A, st);
   GPTQ_LAUNCH_CHECK();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(A.C.heads * A.sets * A.rows), (unsigned)A.count);
