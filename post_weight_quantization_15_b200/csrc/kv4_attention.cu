@@ -24,12 +24,13 @@
 // lanes exchange maxima only when it moves.
 //
 // Work: the sequences' tiles of 32 tokens, all heads, in one line, cut into equal runs, one
-// per block of four warps; a block's warps take its tiles in turn, each with a ring of its
-// own that asynchronous 16-byte copies fill (the codes' pieces swizzled against bank
-// conflicts), so that the warps never wait for each other inside a head.  A head whose tiles
-// fall to one block is finished there; otherwise the blocks leave their (maximum, sum,
-// weighted values) in the workspace and kv4_join_kernel, a dependent launch, joins them in
-// a fixed order.
+// per warp (a head set counts one tile more than it has, for its queries and its end).  A
+// warp has a ring of its own that asynchronous 16-byte copies fill (the codes' pieces
+// swizzled against bank conflicts) and waits for no other warp.  A head set whose tiles
+// fall to one warp is finished there, from registers; of the others, what goes on past a
+// warp's run is joined in the block first, and the blocks' and the last warp's (maximum,
+// sum, weighted values) are left in the workspace, where kv4_join_kernel, a dependent
+// launch, joins them in a fixed order.
 #include <math.h>
 
 #include <climits>
@@ -46,6 +47,8 @@ namespace {
 constexpr int PER_SM = 4;
 constexpr int BLOCKS = 148 * PER_SM;      // resident blocks: the cut of the work, whatever the device
 constexpr int WARPS = 4;
+constexpr int RUNS = BLOCKS * WARPS;
+constexpr int SHORTEST = 4;               // slots of a run, where there are few
 constexpr int TT = 32;                    // tokens of a tile
 constexpr int STAGES = 2;
 constexpr int ROWS = 8;                   // query heads of a product
@@ -59,8 +62,8 @@ struct KvaArgs {
   int64_t q_ts, q_hs, o_ts, o_hs;
   const int32_t* table;
   const int32_t* lengths;
-  float* part_o;                          // [2 BLOCKS][rows][head_dim]
-  float* part_ml;                         // [2 BLOCKS][rows][2]
+  float* part_o;                          // [2 RUNS][rows][head_dim]
+  float* part_ml;                         // [2 RUNS][rows][2]
   int width, count, per, sets, rows;      // per: query heads of a k/v head, in sets of up to 8 (rows)
   float scale;
   int half;                               // q and o are fp16 (else bf16)
@@ -73,38 +76,37 @@ __device__ __forceinline__ int tiles_of(const KvaArgs& A, int b) {
 }
 
 struct Place {
-  int b, hx, t, tiles;                    // sequence, head set, tile of it, tiles of the sequence
-  uint32_t ord;                           // head sets with tiles before this one
+  int b, hx, t, tiles;                    // sequence, head set, tile of it (tiles: none), tiles of the sequence
 };
 
-// Walks the line of tiles with a window of 32 sequences, one per lane.
+// A head set has tiles + 1 slots of the line, the last without a tile.
+__device__ __forceinline__ int64_t slots_of(int tiles, int heads) { return tiles > 0 ? (int64_t)(tiles + 1) * heads : 0; }
+
+// Walks the line of slots with a window of 32 sequences, one per lane.
 struct Finder {
   int b0 = -32;
-  int64_t base = 0, total = 0;            // tiles before and in the window
+  int64_t base = 0, total = 0;            // slots before and in the window
   int64_t incl = 0;                       // this lane's sequence and those before it in the window
-  int tiles = 0, full_before = 0, ones = 0;   // sequences with tiles before the window; up to this lane
+  int tiles = 0;
 
   __device__ __forceinline__ void advance(const KvaArgs& A, int heads) {
     const int lane = threadIdx.x & 31;
-    if (b0 >= 0) full_before += __shfl_sync(0xffffffffu, ones, 31);
     base += total;
     b0 += 32;
     const int b = b0 + lane;
     tiles = b < A.count ? tiles_of(A, b) : 0;
-    incl = (int64_t)tiles * heads;
-    ones = tiles > 0;
+    incl = slots_of(tiles, heads);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
-      const int n = __shfl_up_sync(0xffffffffu, ones, o);
-      if (lane >= o) { incl += up; ones += n; }
+      if (lane >= o) incl += up;
     }
     total = __shfl_sync(0xffffffffu, incl, 31);
   }
 
-  // Each lane's tile (not before the window; lanes without one pass want = -1).
+  // Each lane's slot (not before the window; lanes without one pass want = -1).
   __device__ __forceinline__ Place find(const KvaArgs& A, int heads, int64_t want) {
-    Place p{0, 0, 0, 0, 0};
+    Place p{0, 0, 0, 0};
     bool open = want >= 0;
     while (true) {
       const bool here = open && b0 >= 0 && want < base + total;
@@ -117,14 +119,12 @@ struct Finder {
       }
       const int64_t end = __shfl_sync(0xffffffffu, incl, lo);
       const int n = __shfl_sync(0xffffffffu, tiles, lo);
-      const int k = __shfl_sync(0xffffffffu, ones, lo);
       if (here) {
-        const int64_t r = rel - (end - (int64_t)n * heads);
+        const int64_t r = rel - (end - slots_of(n, heads));
         p.b = b0 + lo;
-        p.hx = (int)(r / n);
-        p.t = (int)(r % n);
+        p.hx = (int)(r / (n + 1));
+        p.t = (int)(r % (n + 1));
         p.tiles = n;
-        p.ord = (uint32_t)(full_before + k - 1) * (uint32_t)heads + (uint32_t)p.hx;
         open = false;
       }
       if (!__any_sync(0xffffffffu, open) || b0 + 32 >= A.count) return p;
@@ -133,16 +133,16 @@ struct Finder {
   }
 };
 
-// Block c's run of the line.
-__device__ __forceinline__ int64_t run_begin(int64_t all, int blocks, int c) { return all * c / blocks; }
-__device__ __forceinline__ int run_of(int64_t all, int blocks, int64_t tile) {
-  int c = (int)(tile * blocks / all);
-  while (c + 1 < blocks && run_begin(all, blocks, c + 1) <= tile) ++c;
+// Run c of the line.
+__device__ __forceinline__ int64_t run_begin(int64_t all, int runs, int c) { return all * c / runs; }
+__device__ __forceinline__ int run_of(int64_t all, int runs, int64_t slot) {
+  int c = (int)(slot * runs / all);
+  while (c + 1 < runs && run_begin(all, runs, c + 1) <= slot) ++c;
   return c;
 }
 __device__ __forceinline__ int runs_of(int64_t all) {
-  const int64_t n = (all + WARPS - 1) / WARPS;
-  return (int)(n < BLOCKS ? n : BLOCKS);
+  const int64_t n = all < SHORTEST ? 1 : all / SHORTEST;
+  return (int)(n < RUNS ? n : RUNS);
 }
 
 template <int D, int GROUP>
@@ -152,11 +152,13 @@ struct KvaSmem {
     __half2 params[2][TT * (D / GROUP)];
   };
   Stage ring[WARPS][STAGES];
-  int4 desc[WARPS][STAGES];               // sequence, head set | pages that exist << 28, first token, ord
-  float out[ROWS][D];
-  float ml[2][WARPS][ROWS][2];
-  int2 seg[2];
+  int4 desc[WARPS][STAGES];               // sequence, head set, first token (-1: no tile), pages that exist
+  float ml[WARPS][ROWS][2];
+  int late[WARPS];                        // the run's last head set goes on behind it (2: and is the only one)
   int skip;
+  // the parts that go on, over the rings when these are done with
+  __device__ __forceinline__ float* part(int w) { return reinterpret_cast<float*>(ring) + w * ROWS * D; }
+  static_assert(sizeof(ring) >= WARPS * ROWS * D * sizeof(float), "parts fit");
 };
 
 // Where 16-byte piece `i` of token row `row` lies in a stage: a row has D / 32 pieces, and
@@ -224,6 +226,31 @@ __device__ __forceinline__ void store_o(const KvaArgs& A, int64_t off, const flo
   else store8(static_cast<__nv_bfloat16*>(A.o) + off, x);
 }
 
+// Eight consecutive features of head 2 j + r from the accumulators (u of D / 64); returns
+// the first feature.  Groups of 32 exchange with the lane four rows on.
+template <int D, int GROUP>
+__device__ __forceinline__ int eight(const float (&acc)[D / 16][4], int r, int u, float (&x)[8]) {
+  const int g = (threadIdx.x & 31) >> 2;
+  if constexpr (GROUP >= 64) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = acc[4 * u + i][r];
+      x[i + 4] = acc[4 * u + i][2 + r];
+    }
+    return 8 * (8 * u + g);
+  } else {
+    const bool odd = g >> 2;              // this lane keeps tile pair 2 u, or 2 u + 1
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float lo = acc[4 * u + (k & 1)][r + (k & 2)], hi = acc[4 * u + 2 + (k & 1)][r + (k & 2)];
+      const float got = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 16), own = odd ? hi : lo;
+      x[2 * k] = odd ? got : own;
+      x[2 * k + 1] = odd ? own : got;
+    }
+    return 8 * (4 * (2 * u + odd) + (g & 3));
+  }
+}
+
 template <int D, int GROUP>
 __global__ void __launch_bounds__(WARPS * 32, PER_SM)
 kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
@@ -238,27 +265,17 @@ kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
   if (threadIdx.x == 0) S.skip = has_error(st);
   const int heads = A.C.heads * A.sets;
   int64_t all = 0;
-  {
-    int64_t mine = 0;
-    for (int b = lane; b < A.count; b += 32) mine += tiles_of(A, b);
+  for (int b = lane; b < A.count; b += 32) all += slots_of(tiles_of(A, b), heads);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    all = mine * heads;
-  }
+  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
   __syncthreads();
-  const int runs = runs_of(all);
-  if (S.skip || (int)blockIdx.x >= runs) return;
-  const int64_t begin = run_begin(all, runs, (int)blockIdx.x), end = run_begin(all, runs, (int)blockIdx.x + 1);
-  Finder finder;
-  const Place ends = finder.find(A, heads, lane == 0 ? begin : (lane == 1 ? end - 1 : -1));
-  const uint32_t ord0 = __shfl_sync(0xffffffffu, ends.ord, 0);
-  const int ord1 = (int)(__shfl_sync(0xffffffffu, ends.ord, 1) - ord0);   // the last head set, from the first
-  const bool from_before = __shfl_sync(0xffffffffu, ends.t, 0) > 0;
-  const bool goes_on = __shfl_sync(0xffffffffu, ends.t + 1 < ends.tiles, 1) != 0;
-  finder = Finder();
+  const int runs = runs_of(all), run = (int)blockIdx.x * WARPS + warp;
+  if (S.skip || all == 0 || run - warp >= runs) return;
+  const int64_t begin = run < runs ? run_begin(all, runs, run) : 0;
+  const int mine = run < runs ? (int)(run_begin(all, runs, run + 1) - begin) : 0;
 
-  // this warp's tiles: begin + warp + 4 i; lane i holds what tile (made & ~31) + i needs
-  const int mine = (int)((end - begin - warp + WARPS - 1) / WARPS);
+  // lane i holds what slot (made & ~31) + i needs
+  Finder finder;
   const int box = min(A.C.page_size, TT), parts = TT / box;      // tokens of a tile in one page; pages of a tile
   int made = 0;
   int64_t row0 = 0, row1 = 0;
@@ -267,9 +284,9 @@ kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
     if (made < mine) {
       if ((made & 31) == 0) {
         const int i = made + lane;
-        const int64_t want = i < mine ? begin + warp + (int64_t)WARPS * i : -1;
-        const Place p = finder.find(A, heads, want);
-        if (want >= 0) {
+        const Place p = finder.find(A, heads, i < mine ? begin + i : -1);
+        d0 = make_int4(0, 0, -1, 0);
+        if (p.t < p.tiles) {
           const int head = p.hx / A.sets, t0 = p.t * TT;
           const int len = A.lengths[p.b];
           int ok = 0;
@@ -293,28 +310,30 @@ kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
             if (k == 0) row0 = row;
             else row1 = page < 0 ? row0 + 16 : row;
           }
-          d0 = make_int4(p.b, p.hx | (ok << 28), t0, (int)(p.ord - ord0));
+          d0 = make_int4(p.b, p.hx, t0, ok);
         }
       }
       const int src = made & 31, s = made % STAGES;
       const int64_t r[2] = {__shfl_sync(0xffffffffu, row0, src), __shfl_sync(0xffffffffu, row1, src)};
       if (lane == src) S.desc[warp][s] = d0;
-      auto& stage = S.ring[warp][s];
+      if (__shfl_sync(0xffffffffu, d0.z, src) >= 0) {
+        auto& stage = S.ring[warp][s];
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        constexpr int P16 = D / 2;        // pieces of 16 tokens
-        const uint32_t dst = smem_addr(stage.codes[kv]) + piece<D>(lane / (D / 32), lane % (D / 32));
-        const char* base = reinterpret_cast<const char*>(A.C.codes[kv]) + lane * 16;
+        for (int kv = 0; kv < 2; ++kv) {
+          constexpr int P16 = D / 2;        // pieces of 16 tokens
+          const uint32_t dst = smem_addr(stage.codes[kv]) + piece<D>(lane / (D / 32), lane % (D / 32));
+          const char* base = reinterpret_cast<const char*>(A.C.codes[kv]) + lane * 16;
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+          for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int i = 0; i < P16 / 32; ++i)    // 32 pieces on, the rows' swizzle repeats
-            copy16(dst + (k * P16 + i * 32) * 16, base + r[k] * (D / 2) + i * 512);
-        constexpr int Q16 = 4 * NG;       // pieces of 16 tokens' scales and zero points
-        if (lane < 2 * Q16) {
-          const int k = lane / Q16;
-          copy16(smem_addr(stage.params[kv]) + lane * 16,
-                 reinterpret_cast<const char*>(A.C.params[kv]) + (k ? r[1] : r[0]) * (NG * 4) + (lane % Q16) * 16);
+            for (int i = 0; i < P16 / 32; ++i)    // 32 pieces on, the rows' swizzle repeats
+              copy16(dst + (k * P16 + i * 32) * 16, base + r[k] * (D / 2) + i * 512);
+          constexpr int Q16 = 4 * NG;       // pieces of 16 tokens' scales and zero points
+          if (lane < 2 * Q16) {
+            const int k = lane / Q16;
+            copy16(smem_addr(stage.params[kv]) + lane * 16,
+                   reinterpret_cast<const char*>(A.C.params[kv]) + (k ? r[1] : r[0]) * (NG * 4) + (lane % Q16) * 16);
+          }
         }
       }
       ++made;
@@ -330,9 +349,19 @@ kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
   int ve[NG];                             // weights of group i carry 2^(10 - ve[i])
   uint32_t qb[D / 16][2];                 // head g's query as operand
   float rf[2] = {1.f, 1.f};               // log2 of a weight per unit of score
-  int used = 0, cur = -1, at_b = 0, at_hx = 0;
+  int used = 0, sets = 0, late = 0;
 
-  for (int ord = 0; ord <= ord1; ++ord) {
+  while (used < mine) {
+    const int4 begins = S.desc[warp][used % STAGES];
+    if (begins.z < 0) {                   // a slot without a tile
+      __syncwarp();
+      ++used;
+      produce();
+      __syncwarp();
+      continue;
+    }
+    const int b = begins.x, hx = begins.y, len = A.lengths[b];
+    const int first = hx / A.sets * A.per + (hx % A.sets) * ROWS, rows = min(ROWS, A.per - (hx % A.sets) * ROWS);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -341,52 +370,46 @@ kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
     for (int i = 0; i < NG; ++i) ve[i] = -127;
     m[0] = m[1] = -INFINITY;
     l[0] = l[1] = 0.f;
-
+    {                                     // its queries as operands
+      float x[NW][8];
+      float top = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const int word = NG == 1 ? NW * j + w : j + 4 * w;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[w][e] = 0.f;
+        if (g < rows) load_q(A, (int64_t)b * A.q_ts + (int64_t)(first + g) * A.q_hs + word * 8, x[w]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[w][e]));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int e2 = top > 0.f && top <= 3.4028235e38f ? ilogbf(top) : 0;
+      // a scale below 0 goes to the queries; one of 0 (or scores that vanish in fp32) makes them 0
+      float f = ldexpf(fabsf(A.scale) * LOG2E, e2 - 11);
+      const float sign = f == 0.f ? 0.f : (A.scale < 0.f ? -1.f : 1.f);
+      f = f == 0.f ? 1.f : f;
+      rf[0] = __shfl_sync(0xffffffffu, f, 8 * j);
+      rf[1] = __shfl_sync(0xffffffffu, f, 8 * j + 4);
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[w][e] = ldexpf(x[w][e], 11 - e2) * sign;
+        // a word's codes come in the pairs (i, i + 4)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          qb[2 * w + k][0] = pack2(x[w][2 * k], x[w][2 * k + 4], __half());
+          qb[2 * w + k][1] = pack2(x[w][2 * k + 1], x[w][2 * k + 5], __half());
+        }
+      }
+    }
+    int t0 = 0;
     while (used < mine) {
       const int s = used % STAGES;
       const int4 d = S.desc[warp][s];
-      if (d.w != ord) break;
-      const int b = d.x, hx = d.y & 0x0fffffff, ok = (int)((uint32_t)d.y >> 28), t0 = d.z;
-      const int have = A.lengths[b] - t0;
-      if (cur != ord) {
-        // this warp's first tile of the head set: its queries as operands
-        cur = ord;
-        at_b = b;
-        at_hx = hx;
-        const int head = hx / A.sets, first = head * A.per + (hx % A.sets) * ROWS;
-        const int rows = min(ROWS, A.per - (hx % A.sets) * ROWS);
-        float x[NW][8];
-        float top = 0.f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const int word = NG == 1 ? NW * j + w : j + 4 * w;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[w][e] = 0.f;
-          if (g < rows) load_q(A, (int64_t)b * A.q_ts + (int64_t)(first + g) * A.q_hs + word * 8, x[w]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[w][e]));
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e2 = top > 0.f && top <= 3.4028235e38f ? ilogbf(top) : 0;
-        // a scale below 0 goes to the queries; one of 0 (or scores that vanish in fp32) makes them 0
-        float f = ldexpf(fabsf(A.scale) * LOG2E, e2 - 11);
-        const float sign = f == 0.f ? 0.f : (A.scale < 0.f ? -1.f : 1.f);
-        f = f == 0.f ? 1.f : f;
-        rf[0] = __shfl_sync(0xffffffffu, f, 8 * j);
-        rf[1] = __shfl_sync(0xffffffffu, f, 8 * j + 4);
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[w][e] = ldexpf(x[w][e], 11 - e2) * sign;
-          // a word's codes come in the pairs (i, i + 4)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            qb[2 * w + k][0] = pack2(x[w][2 * k], x[w][2 * k + 4], __half());
-            qb[2 * w + k][1] = pack2(x[w][2 * k + 1], x[w][2 * k + 5], __half());
-          }
-        }
-      }
+      if (d.z < 0) break;                 // the head set's end
+      t0 = d.z;
+      const int ok = d.w, have = len - t0;
       const bool edge = have < TT || ok != 3;
       asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
       __syncwarp();
@@ -565,72 +588,91 @@ kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
       __syncwarp();                       // the next tiles' descriptors are there
     }
 
-    // ---- the four warps' parts of this head set joined, in order ----
-    float (*ml)[ROWS][2] = S.ml[ord & 1];
+    // ---- its end ----
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-      if (g == 0) {
-        ml[warp][2 * j + r][0] = m[r];
-        ml[warp][2 * j + r][1] = l[r];
-      }
+#pragma unroll
+    for (int a = 0; a < MT; ++a) {
+      const int i = a * NG / MT;
+      const float mul = ve[i] < -116 ? 0.f : __uint_as_float((uint32_t)(ve[i] - 10 + 127) << 23);   // unset: acc is 0
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[a][e] *= mul;
     }
-    if (cur == ord && lane == 0) S.seg[ord & 1] = make_int2(at_b, at_hx);
-    __syncthreads();
-    const int b = S.seg[ord & 1].x, hx = S.seg[ord & 1].y;
-    const int first = hx / A.sets * A.per + (hx % A.sets) * ROWS, rows = min(ROWS, A.per - (hx % A.sets) * ROWS);
-    float f[2];
+    ++sets;
+    const bool early = begins.z > 0;
+    if (used == mine && len - t0 > TT) {
+      late = early && sets == 1 ? 2 : 1;
+      break;
+    }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      float top = -INFINITY;
+      const int row = 2 * j + r;
+      const float inv = m[r] == -INFINITY ? 0.f : 1.f / l[r];
+      const int64_t at = (int64_t)(2 * run) * A.rows + row;
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w][2 * j + r][0]);
-      f[r] = m[r] == -INFINITY ? 0.f : ex2(m[r] - top);
-    }
-    for (int w = 0; w < WARPS; ++w) {
-      if (warp == w) {
+      for (int u = 0; u < D / 64; ++u) {
+        float x[8];
+        const int dim = eight<D, GROUP>(acc, r, u, x);
+        if (row < rows) {
+          if (early) {
+            store8(A.part_o + at * D + dim, x);
+          } else {
 #pragma unroll
-        for (int a = 0; a < MT; ++a) {
-          const int i = a * NG / MT;
-          const float mul = ve[i] < -116 ? 0.f : __uint_as_float((uint32_t)(ve[i] - 10 + 127) << 23);   // unset: acc is 0
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int head = 2 * j + (e & 1), up = (e >> 1) * 4;
-            const int dim = GROUP >= 64 ? 8 * (8 * (a / 4) + g) + a % 4 + up
-                                        : 8 * (4 * (a / 2) + (g & 3)) + 2 * (a % 2) + (g >> 2) + up;
-            const float v = acc[a][e] * mul * f[e & 1];
-            S.out[head][dim] = w == 0 ? v : S.out[head][dim] + v;
+            for (int e = 0; e < 8; ++e) x[e] *= inv;
+            store_o(A, (int64_t)b * A.o_ts + (int64_t)(first + row) * A.o_hs + dim, x);
           }
         }
       }
-      __syncthreads();
+      if (early && row < rows && g == 0) {
+        A.part_ml[at * 2] = m[r];
+        A.part_ml[at * 2 + 1] = l[r];
+      }
     }
-    const bool early = ord == 0 && from_before, late = ord == ord1 && goes_on;
-    const int slot = 2 * (int)blockIdx.x + (early ? 0 : 1);
-    for (int u = (int)threadIdx.x; u < rows * (D / 8); u += WARPS * 32) {
+  }
+
+  // ---- what goes on behind the warps' runs, joined where it is one head set ----
+  if (lane == 0) S.late[warp] = late;
+  __syncthreads();                        // every warp is done with its ring
+  if (late) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = 2 * j + r;
+#pragma unroll
+      for (int u = 0; u < D / 64; ++u) {
+        float x[8];
+        const int dim = eight<D, GROUP>(acc, r, u, x);
+        if (row < A.rows) store8(S.part(warp) + row * D + dim, x);
+      }
+      if (g == 0) {
+        S.ml[warp][row][0] = m[r];
+        S.ml[warp][row][1] = l[r];
+      }
+    }
+  }
+  __syncthreads();
+  for (int w0 = 0, w1; w0 < WARPS; w0 = w1) {
+    w1 = w0 + 1;
+    if (!S.late[w0]) continue;
+    while (w1 < WARPS && S.late[w1] == 2) ++w1;
+    for (int u = (int)threadIdx.x; u < A.rows * (D / 8); u += WARPS * 32) {
       const int row = u / (D / 8), c8 = u % (D / 8);
-      float top = -INFINITY, sum = 0.f;
+      float top = -INFINITY, sum = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      for (int w = w0; w < w1; ++w) top = fmaxf(top, S.ml[w][row][0]);
+      for (int w = w0; w < w1; ++w) {
+        if (S.ml[w][row][0] == -INFINITY) continue;
+        const float f = ex2(S.ml[w][row][0] - top);
+        sum = fmaf(S.ml[w][row][1], f, sum);
+        const float* o = S.part(w) + row * D + c8 * 8;
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w][row][0]);
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w)
-        if (ml[w][row][0] != -INFINITY) sum += ml[w][row][1] * ex2(ml[w][row][0] - top);
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = S.out[row][c8 * 8 + e];
-      if (!early && !late) {
-        const float inv = top == -INFINITY ? 0.f : 1.f / sum;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= inv;
-        store_o(A, (int64_t)b * A.o_ts + (int64_t)(first + row) * A.o_hs + c8 * 8, x);
-      } else {
-        const int64_t at = (int64_t)slot * A.rows + row;
-        store8(A.part_o + at * D + c8 * 8, x);
-        if (c8 == 0) {
-          A.part_ml[at * 2] = top;
-          A.part_ml[at * 2 + 1] = sum;
-        }
+        for (int e = 0; e < 8; ++e) x[e] = fmaf(o[e], f, x[e]);
+      }
+      const int64_t at = (int64_t)(2 * (run - warp + w0) + 1) * A.rows + row;
+      store8(A.part_o + at * D + c8 * 8, x);
+      if (c8 == 0) {
+        A.part_ml[at * 2] = top;
+        A.part_ml[at * 2 + 1] = sum;
       }
     }
   }
@@ -649,7 +691,7 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ K
   const int heads = A.C.heads * A.sets;
   long long before = 0, all = 0;
   for (int i = (int)threadIdx.x; i < A.count; i += 256) {
-    const int n = tiles_of(A, i);
+    const int64_t n = slots_of(tiles_of(A, i), heads);
     all += n;
     if (i < b) before += n;
   }
@@ -679,17 +721,19 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ K
     if (threadIdx.x < D / 8) store_o(A, at + threadIdx.x * 8, zero);
     return;
   }
-  all *= heads;
   const int runs = runs_of(all);
-  const int64_t t0 = before * heads + (int64_t)hx * n, t1 = t0 + n - 1;
+  const int64_t t0 = before + (int64_t)hx * (n + 1), t1 = t0 + n - 1;
   const int c0 = run_of(all, runs, t0), c1 = run_of(all, runs, t1);
-  if (c0 == c1) return;                   // finished by its block
+  if (c0 == c1) return;                   // finished by its warp
+  // the parts: run c0's, those of the blocks after it (their first run's), and the last run's
+  const int parts = 2 + (c1 - 1) / WARPS - c0 / WARPS;
   float m = -INFINITY, l = 0.f, x[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) x[e] = 0.f;
 #pragma unroll 4
-  for (int c = c0 + warp; c <= c1; c += 8) {
-    const int64_t p = (int64_t)(2 * c + (c == c0 ? 1 : 0)) * A.rows + row;
+  for (int i = warp; i < parts; i += 8) {
+    const int64_t slot = i == parts - 1 ? 2 * c1 : 2 * (i == 0 ? c0 : (c0 / WARPS + i) * WARPS) + 1;
+    const int64_t p = slot * A.rows + row;
     const float pm = A.part_ml[p * 2], pl = A.part_ml[p * 2 + 1];
     const float mn = fmaxf(m, pm), ref = mn == -INFINITY ? 0.f : mn;
     const float f = ex2(m - ref), w = ex2(pm - ref);
@@ -745,7 +789,7 @@ int launch(const KvaArgs& A, int32_t* st, cudaStream_t s) {
 }  // namespace
 
 size_t kv4_attention_ws_bytes(int, int heads_q, int heads_kv, int head_dim, int64_t) {
-  return (size_t)2 * BLOCKS * set_rows(heads_q / heads_kv) * (head_dim + 2) * sizeof(float);
+  return (size_t)2 * RUNS * set_rows(heads_q / heads_kv) * (head_dim + 2) * sizeof(float);
 }
 
 int launch_kv4_attention(const KV4Cache& C, const void* q, int64_t q_ts, int64_t q_hs, int dtype, int count,
@@ -753,7 +797,7 @@ int launch_kv4_attention(const KV4Cache& C, const void* q, int64_t q_ts, int64_t
                          int64_t o_ts, int64_t o_hs, void* ws, int32_t* st, cudaStream_t s) {
   const int per = heads_q / C.heads, rows = set_rows(per);
   KvaArgs A{C, q, o, q_ts, q_hs, o_ts, o_hs, table, lengths, static_cast<float*>(ws),
-            static_cast<float*>(ws) + (size_t)2 * BLOCKS * rows * C.head_dim, width, count, per, head_sets(per), rows,
+            static_cast<float*>(ws) + (size_t)2 * RUNS * rows * C.head_dim, width, count, per, head_sets(per), rows,
             scale, dtype == GPTQ_F16};
   TraceScope ts("kv4_attention", "", 0.0, s);
   if (C.head_dim == 64) return C.group == 32 ? launch<64, 32>(A, st, s) : launch<64, 64>(A, st, s);
