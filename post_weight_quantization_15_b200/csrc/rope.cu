@@ -7,10 +7,12 @@
 // pairs being (i, i + rot/2) of a head, or (2i, 2i + 1) when interleaved; features from
 // rot on and all of v pass through.  The tables hold the cosines and sines per position.
 //
-// Bound: HBM (4 bytes in, 2 out per value).  One pass, W pairs per thread: 16 values read
-// as 16-byte pieces and written as two of them (W = 8); W = 4 where rot or the head size
-// asks for it, W = 1 for any even rot and any alignment.  A block stays within one token,
-// whose table rows its heads share in L1.
+// Bound: HBM (4 bytes in, 2 out per value).  One pass.  A thread keeps the same W pairs of
+// every head it takes, so that their cosines and sines are read once into registers and a
+// head costs two 16-byte loads (W = 4 of fp32, 8 of 16-bit types, side by side across a
+// warp) and two stores; W = 1 for any even rot and any alignment.  A block stays within one
+// token.  (A unit of 16 values per thread with the tables read again for every head took
+// 190 us for 8192 tokens of 96 heads x 128 where this one takes 117.)
 #include "common.cuh"
 #include "internal.h"
 #include "vec_io.cuh"
@@ -18,6 +20,9 @@
 namespace gptq {
 
 namespace {
+
+constexpr int THREADS = 256;
+constexpr int ENOUGH = 148 * 4;           // blocks that fill the SMs
 
 struct RopeArgs {
   const void* X;
@@ -46,82 +51,102 @@ __device__ __forceinline__ void storew(T* p, const float (&v)[W]) {
   else store_from_float(p, v[0]);
 }
 
-// Thread: 2 W values of one head of one token; a head has d / (2 W) such units (W = 1:
-// rot and d even), the first rot / (2 W) of them rotated in q and k heads.
-template <typename TX, typename TO, int W>
-__global__ void __launch_bounds__(256) rope_qkv_kernel(const RopeArgs A, int units, int32_t* st) {
+// Thread: pairs j W .. j W + W - 1 of heads h0, h0 + step, ...; a head has `units` = d / (2 W)
+// such pieces (W = 1: rot and d even), the first rot / (2 W) of them rotated in q and k heads.
+template <typename TX, typename TO, int W, bool BIAS>
+__global__ void __launch_bounds__(THREADS)
+rope_qkv_kernel(const __grid_constant__ RopeArgs A, int units, int per_block, int32_t* st) {
   if (has_error(st)) return;
   const int t = (int)blockIdx.x;
-  const int heads = A.hq + 2 * A.hk;
+  const int turned = A.hq + A.hk, heads = turned + A.hk;
+  const int sub = (int)threadIdx.x / units, subs = max(1, min(THREADS / units, per_block));
+  const int begin = (int)blockIdx.y * per_block, end = min(heads, begin + per_block);
+  if (sub >= subs) return;
   int pos = A.positions != nullptr ? A.positions[t] : t;
   if (A.rot > 0 && (pos < 0 || pos >= A.max_pos)) {
     if (threadIdx.x == 0 && blockIdx.y == 0) set_error(st, GPTQ_ERR_INVALID_ARG, t, STAGE_ROPE);
     pos = 0;
   }
-  const TX* row = static_cast<const TX*>(A.X) + (int64_t)t * A.ld;
-  for (int u = (int)blockIdx.y * 256 + (int)threadIdx.x; u < heads * units; u += 256 * (int)gridDim.y) {
-    const int head = u / units, j = u % units;
-    const bool turn = head < A.hq + A.hk && j * 2 * W < A.rot;
-    // the unit's two runs of W values inside the head
+  for (int j = (int)threadIdx.x % units; j < units; j += THREADS) {      // units above the block's threads: W = 1 only
+    const bool turn = j * 2 * W < A.rot;
+    // the piece's two runs of W values inside a head
     const bool split = turn && !A.interleaved;
     const int i0 = split ? j * W : j * 2 * W;
     const int i1 = split ? j * W + A.rot / 2 : j * 2 * W + W;
-    const int c0 = head * A.d + i0, c1 = head * A.d + i1;
-    float a[W], b[W];
-    loadw<W>(row + c0, a);
-    loadw<W>(row + c1, b);
-    if (A.bias != nullptr) {
-#pragma unroll
-      for (int i = 0; i < W; ++i) {
-        a[i] += A.bias[c0 + i];
-        b[i] += A.bias[c1 + i];
-      }
-    }
+    float c[W], s[W];
     if (turn) {
-      const float* cs = A.cos + (int64_t)pos * (A.rot / 2) + j * W;
-      const float* sn = A.sin + (int64_t)pos * (A.rot / 2) + j * W;
-      float c[W], s[W];
-      loadw<W>(cs, c);
-      loadw<W>(sn, s);
-      if (A.interleaved) {
-        // pair i of the unit: values 2i and 2i + 1 of the 2 W consecutive ones
-        float x[2 * W];
-#pragma unroll
-        for (int i = 0; i < W; ++i) { x[i] = a[i]; x[W + i] = b[i]; }
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-          const float lo = x[2 * i], hi = x[2 * i + 1];
-          x[2 * i] = lo * c[i] - hi * s[i];
-          x[2 * i + 1] = lo * s[i] + hi * c[i];
-        }
-#pragma unroll
-        for (int i = 0; i < W; ++i) { a[i] = x[i]; b[i] = x[W + i]; }
-      } else {
+      loadw<W>(A.cos + (int64_t)pos * (A.rot / 2) + j * W, c);
+      loadw<W>(A.sin + (int64_t)pos * (A.rot / 2) + j * W, s);
+    }
+    const TX* row = static_cast<const TX*>(A.X) + (int64_t)t * A.ld;
+#pragma unroll 4
+    for (int head = begin + sub; head < end; head += subs) {
+      const int c0 = head * A.d + i0, c1 = head * A.d + i1;
+      float a[W], b[W];
+      loadw<W>(row + c0, a);
+      loadw<W>(row + c1, b);
+      if constexpr (BIAS) {
+        float x[W], y[W];
+        loadw<W>(A.bias + c0, x);
+        loadw<W>(A.bias + c1, y);
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-          const float lo = a[i], hi = b[i];
-          a[i] = lo * c[i] - hi * s[i];
-          b[i] = lo * s[i] + hi * c[i];
+          a[i] += x[i];
+          b[i] += y[i];
         }
       }
+      if (turn && head < turned) {
+        if (A.interleaved) {
+          // pair i of the piece: values 2i and 2i + 1 of the 2 W consecutive ones
+          float x[2 * W];
+#pragma unroll
+          for (int i = 0; i < W; ++i) { x[i] = a[i]; x[W + i] = b[i]; }
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            const float lo = x[2 * i], hi = x[2 * i + 1];
+            x[2 * i] = lo * c[i] - hi * s[i];
+            x[2 * i + 1] = lo * s[i] + hi * c[i];
+          }
+#pragma unroll
+          for (int i = 0; i < W; ++i) { a[i] = x[i]; b[i] = x[W + i]; }
+        } else {
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            const float lo = a[i], hi = b[i];
+            a[i] = lo * c[i] - hi * s[i];
+            b[i] = lo * s[i] + hi * c[i];
+          }
+        }
+      }
+      TO* dst;
+      if (head < A.hq) dst = static_cast<TO*>(A.q) + ((int64_t)t * A.hq + head) * A.d;
+      else if (head < turned) dst = static_cast<TO*>(A.k) + ((int64_t)t * A.hk + head - A.hq) * A.d;
+      else dst = static_cast<TO*>(A.v) + ((int64_t)t * A.hk + head - turned) * A.d;
+      storew<W>(dst + i0, a);
+      storew<W>(dst + i1, b);
     }
-    TO* dst;
-    if (head < A.hq) dst = static_cast<TO*>(A.q) + ((int64_t)t * A.hq + head) * A.d;
-    else if (head < A.hq + A.hk) dst = static_cast<TO*>(A.k) + ((int64_t)t * A.hk + head - A.hq) * A.d;
-    else dst = static_cast<TO*>(A.v) + ((int64_t)t * A.hk + head - A.hq - A.hk) * A.d;
-    storew<W>(dst + i0, a);
-    storew<W>(dst + i1, b);
   }
+}
+
+template <typename TX, typename TO, int W>
+void launch_w(const RopeArgs& A, int32_t* st, cudaStream_t s) {
+  const int units = A.d / (2 * W), heads = A.hq + 2 * A.hk;
+  const int subs = THREADS / units > 0 ? THREADS / units : 1;
+  // few tokens: a head per thread; else one block per token
+  const int64_t want = cdiv(heads, subs);
+  const int64_t split = A.tokens >= ENOUGH ? 1 : (want < 64 ? want : 64);
+  const int per_block = (int)cdiv(heads, split);
+  const dim3 grd((unsigned)A.tokens, (unsigned)cdiv(heads, per_block));
+  if (A.bias != nullptr) rope_qkv_kernel<TX, TO, W, true><<<grd, THREADS, 0, s>>>(A, units, per_block, st);
+  else rope_qkv_kernel<TX, TO, W, false><<<grd, THREADS, 0, s>>>(A, units, per_block, st);
 }
 
 template <typename TX, typename TO>
 void launch(const RopeArgs& A, int w, int32_t* st, cudaStream_t s) {
-  const int units = A.d / (2 * w);
-  const int64_t all = (int64_t)(A.hq + 2 * A.hk) * units;
-  const dim3 grd((unsigned)A.tokens, (unsigned)(cdiv(all, 256) < 64 ? cdiv(all, 256) : 64));
-  if (w == 8) rope_qkv_kernel<TX, TO, 8><<<grd, 256, 0, s>>>(A, units, st);
-  else if (w == 4) rope_qkv_kernel<TX, TO, 4><<<grd, 256, 0, s>>>(A, units, st);
-  else rope_qkv_kernel<TX, TO, 1><<<grd, 256, 0, s>>>(A, units, st);
+  if constexpr (sizeof(TX) == 2)
+    if (w == 8) { launch_w<TX, TO, 8>(A, st, s); return; }
+  if (w >= 4) launch_w<TX, TO, 4>(A, st, s);
+  else launch_w<TX, TO, 1>(A, st, s);
 }
 
 template <typename TX>
@@ -139,9 +164,10 @@ int launch_rope_qkv(const void* X, int x_dtype, int64_t ld, const float* bias, c
                     int d, int out_dtype, void* q, void* k, void* v, int32_t* st, cudaStream_t s) {
   RopeArgs A{X, ld, bias, cos, sin, positions, max_pos, rot, interleaved, tokens, hq, hk, d, q, k, v};
   const int xb = x_dtype == GPTQ_F32 ? 4 : 2;
-  const bool al = al16(X) && (ld * xb) % 16 == 0 && al16(q) && al16(k) && al16(v) && (rot == 0 || (al16(cos) && al16(sin)));
+  const bool al = al16(X) && (ld * xb) % 16 == 0 && al16(q) && al16(k) && al16(v) && (rot == 0 || (al16(cos) && al16(sin))) &&
+                  (bias == nullptr || al16(bias));
   int w = 1;
-  if (al && rot % 16 == 0 && d % 16 == 0) w = 8;
+  if (al && rot % 16 == 0 && d % 16 == 0 && xb == 2) w = 8;
   else if (al && rot % 8 == 0 && d % 8 == 0) w = 4;
   const double cols = (double)(hq + 2 * hk) * d;
   TraceScope ts("rope_qkv", "byte", tokens * (cols * (xb + 2) + 4.0 * rot), s);
