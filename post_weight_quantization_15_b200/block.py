@@ -15,37 +15,54 @@ streams that made the inputs.  What a call allocates belongs to the stream it la
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import dataclasses
 from typing import Optional, Tuple
 
 import torch
 
-from .gptq import _DTYPE_CODE, _KV4, _check, _ptr, _require_cuda, lib, workspace
+from .gptq import _DTYPE_CODE, _KV4, _check, _require_cuda, lib, workspace
 
 _16BIT = (torch.float16, torch.bfloat16)
 
 
-@contextlib.contextmanager
-def _launching(stream, *ts: Optional[torch.Tensor]):
-    """The call's device made current, and its stream (as a pointer); allocations go to that stream."""
-    _require_cuda(*ts)
-    dev = next(t.device for t in ts if t is not None)
-    for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError("all tensors must be on one device")
-    if stream is None:
-        if dev.index == torch.cuda.current_device():
-            yield ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
-            return
-        with torch.cuda.device(dev):
-            yield ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
-        return
-    if stream.device != dev:
-        raise ValueError("stream must be on the tensors' device")
-    with torch.cuda.stream(stream):
-        yield ctypes.c_void_p(stream.cuda_stream)
+class _Launching:
+    """With the call's device and stream current (allocations go to that stream): the stream's pointer.
+
+    A call on the current device's current stream, the usual one, changes and restores nothing."""
+    __slots__ = ("ptr", "cm")
+
+    def __init__(self, stream, first: torch.Tensor, *ts: Optional[torch.Tensor]):
+        dev = first.get_device()
+        if dev < 0:
+            _require_cuda(first)
+        for t in ts:
+            if t is not None and t.get_device() != dev:
+                _require_cuda(t)
+                raise ValueError("all tensors must be on one device")
+        self.cm = None
+        if stream is not None:
+            if stream.device.index != dev:
+                raise ValueError("stream must be on the tensors' device")
+            self.ptr = stream.cuda_stream
+            self.cm = torch.cuda.stream(stream)
+        else:
+            self.ptr = torch._C._cuda_getCurrentRawStream(dev)
+            if dev != torch.cuda.current_device():
+                self.cm = torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.cm is not None:
+            self.cm.__enter__()
+        return self.ptr
+
+    def __exit__(self, *exc):
+        if self.cm is not None:
+            self.cm.__exit__(*exc)
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _status_ok(status: Optional[torch.Tensor]):
@@ -74,9 +91,10 @@ def _apart(out: Optional[torch.Tensor], *ins: Optional[torch.Tensor]):
 
 
 def _rows(t: torch.Tensor, tokens: int, d: int, what: str):
-    if t.dim() != 2 or tuple(t.shape) != (tokens, d) or t.dtype not in _DTYPE_CODE or (d > 1 and t.stride(1) != 1) \
-            or (tokens > 1 and t.stride(0) < d):
-        raise ValueError(f"{what} must be an fp32/fp16/bf16 [{tokens}, {d}] tensor with contiguous rows")
+    if t.dtype in _DTYPE_CODE and t.shape == (tokens, d):
+        if t.is_contiguous() or ((d == 1 or t.stride(1) == 1) and (tokens == 1 or t.stride(0) >= d)):
+            return
+    raise ValueError(f"{what} must be an fp32/fp16/bf16 [{tokens}, {d}] tensor with contiguous rows")
 
 
 def _ld(t: Optional[torch.Tensor], d: int) -> int:
@@ -85,7 +103,7 @@ def _ld(t: Optional[torch.Tensor], d: int) -> int:
 
 
 def _ints(t: torch.Tensor, shape, what: str):
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)}")
 
 
@@ -117,7 +135,7 @@ def add_norm(X: torch.Tensor, weight: torch.Tensor, Y: Optional[torch.Tensor] = 
     if weight.dtype not in _DTYPE_CODE:
         raise ValueError("weight must be fp32/fp16/bf16")
     for t, what in ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight"), (post_bias, "post_bias")):
-        if t is not None and (tuple(t.shape) != (d,) or t.dtype != weight.dtype or not t.is_contiguous()):
+        if t is not None and (t.shape != (d,) or t.dtype != weight.dtype or not t.is_contiguous()):
             raise ValueError(f"{what} must be a contiguous [{d}] tensor of weight's type")
     ld_gate = 0
     if gate is not None:
@@ -129,25 +147,26 @@ def add_norm(X: torch.Tensor, weight: torch.Tensor, Y: Optional[torch.Tensor] = 
         elif tuple(gate.shape) != (d,) or not gate.is_contiguous():
             raise ValueError(f"gate must be a contiguous [{d}] or a [{tokens}, {d}] tensor")
     _status_ok(status)
-    with _launching(stream, X, weight, Y, post_weight, gate, bias, post_bias, x_out, out, status) as s:
+    with _Launching(stream, X, weight, Y, post_weight, gate, bias, post_bias, x_out, out, status) as s:
+        given = [t for t in (out, x_out) if t is not None]
         if out is None:
-            out = torch.empty((tokens, d), dtype=X.dtype, device=X.device)
+            out = torch.empty_like(X, memory_format=torch.contiguous_format)
         if Y is not None and x_out is None:
-            x_out = torch.empty((tokens, d), dtype=X.dtype, device=X.device)
-        for t, what in ((out, "out"), (x_out, "x_out")):
-            if t is not None:
-                _rows(t, tokens, d, what)
+            x_out = torch.empty_like(X, memory_format=torch.contiguous_format)
+        if given:                         # what was allocated here fits and lies apart
+            for t in given:
+                _rows(t, tokens, d, "out" if t is out else "x_out")
                 if t.dtype != X.dtype:
-                    raise ValueError(f"{what} must have X's type")
-        par = (weight, bias, post_weight, post_bias, gate)
-        _apart(out, X, Y, x_out, *par)
-        same = x_out is not None and x_out.data_ptr() == X.data_ptr() and _ld(x_out, d) == _ld(X, d)
-        _apart(x_out, None if same else X, Y, *par)
-        _check(lib().gptq_add_norm(_ptr(X), _DTYPE_CODE[X.dtype], _ld(X, d), _ptr(Y),
-                                   _DTYPE_CODE[Y.dtype if Y is not None else X.dtype], _ld(Y, d), _ptr(weight),
-                                   _ptr(bias), _ptr(post_weight), _ptr(post_bias), _ptr(gate), ld_gate,
+                    raise ValueError("out and x_out must have X's type")
+            par = (weight, bias, post_weight, post_bias, gate)
+            _apart(out, X, Y, x_out, *par)
+            same = x_out is not None and x_out.data_ptr() == X.data_ptr() and _ld(x_out, d) == _ld(X, d)
+            _apart(x_out, None if same else X, Y, *par)
+        _check(lib().gptq_add_norm(_at(X), _DTYPE_CODE[X.dtype], _ld(X, d), _at(Y),
+                                   _DTYPE_CODE[Y.dtype if Y is not None else X.dtype], _ld(Y, d), _at(weight),
+                                   _at(bias), _at(post_weight), _at(post_bias), _at(gate), ld_gate,
                                    _DTYPE_CODE[weight.dtype], tokens, d, float(alpha), float(eps), int(bool(center)),
-                                   _ptr(x_out), _ld(x_out, d), _ptr(out), _ld(out, d), _ptr(status), s),
+                                   _at(x_out), _ld(x_out, d), _at(out), _ld(out, d), _at(status), s),
                "gptq_add_norm")
     return (X if Y is None else x_out), out
 
@@ -182,13 +201,13 @@ def rope_qkv(QKV: torch.Tensor, cos: Optional[torch.Tensor], sin: Optional[torch
     if positions is not None:
         _ints(positions, (tokens,), "positions")
     _status_ok(status)
-    with _launching(stream, QKV, cos, sin, positions, bias, status) as s:
+    with _Launching(stream, QKV, cos, sin, positions, bias, status) as s:
         q = torch.empty((tokens, heads_q, head_dim), dtype=dtype, device=QKV.device)
         k = torch.empty((tokens, heads_kv, head_dim), dtype=dtype, device=QKV.device)
         v = torch.empty((tokens, heads_kv, head_dim), dtype=dtype, device=QKV.device)
-        _check(lib().gptq_rope_qkv(_ptr(QKV), _DTYPE_CODE[QKV.dtype], _ld(QKV, cols), _ptr(bias), _ptr(cos),
-                                   _ptr(sin), max_pos, rot, int(bool(interleaved)), _ptr(positions), tokens, heads_q,
-                                   heads_kv, head_dim, _DTYPE_CODE[dtype], _ptr(q), _ptr(k), _ptr(v), _ptr(status),
+        _check(lib().gptq_rope_qkv(_at(QKV), _DTYPE_CODE[QKV.dtype], _ld(QKV, cols), _at(bias), _at(cos),
+                                   _at(sin), max_pos, rot, int(bool(interleaved)), _at(positions), tokens, heads_q,
+                                   heads_kv, head_dim, _DTYPE_CODE[dtype], _at(q), _at(k), _at(v), _at(status),
                                    s), "gptq_rope_qkv")
     return q, k, v
 
@@ -204,8 +223,10 @@ def _heads(t: torch.Tensor, dtype, what: str):
 def _strides(t: torch.Tensor):
     """Token and head strides; those of a single token or head are not used."""
     n, h, d = t.shape
-    hs = t.stride(1) if h > 1 else d
-    return (t.stride(0) if n > 1 else h * hs), hs
+    ts, hs, _ = t.stride()
+    if h == 1:
+        hs = d
+    return (ts if n > 1 else h * hs), hs
 
 
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
@@ -232,17 +253,18 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Ten
     _ints(cu_q, cu_q.shape, "cu_q")
     _ints(cu_k, cu_q.shape, "cu_k")
     _status_ok(status)
-    with _launching(stream, q, k, v, cu_q, cu_k, out, status) as s:
+    with _Launching(stream, q, k, v, cu_q, cu_k, out, status) as s:
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        _heads(out, q.dtype, "out")
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
-        _apart(out, q, k, v)
-        _check(lib().gptq_attention(_ptr(q), *_strides(q), _ptr(k), *_strides(k), _ptr(v), *_strides(v),
-                                    _DTYPE_CODE[q.dtype], _ptr(cu_q), _ptr(cu_k), cu_q.numel() - 1, q.shape[0],
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        else:
+            _heads(out, q.dtype, "out")
+            if out.shape != q.shape:
+                raise ValueError("out must have q's shape")
+            _apart(out, q, k, v)
+        _check(lib().gptq_attention(_at(q), *_strides(q), _at(k), *_strides(k), _at(v), *_strides(v),
+                                    _DTYPE_CODE[q.dtype], _at(cu_q), _at(cu_k), cu_q.numel() - 1, q.shape[0],
                                     k.shape[0], hq, hk, d, float(d ** -0.5 if scale is None else scale),
-                                    int(bool(causal)), _ptr(out), *_strides(out), _ptr(status), s), "gptq_attention")
+                                    int(bool(causal)), _at(out), *_strides(out), _at(status), s), "gptq_attention")
     return out
 
 
@@ -273,11 +295,11 @@ def _cache(c: KV4Cache) -> _KV4:
     d = words * 8
     if c.group < 1 or d % c.group:
         raise ValueError("group must divide head_dim")
+    shape, pshape = c.k_codes.shape, (pages, heads, page, d // c.group, 2)
     for codes, par in ((c.k_codes, c.k_params), (c.v_codes, c.v_params)):
-        if codes.dtype != torch.int32 or codes.shape != c.k_codes.shape or not codes.is_contiguous():
+        if codes.dtype != torch.int32 or codes.shape != shape or not codes.is_contiguous():
             raise ValueError("codes must be contiguous int32 tensors of one shape")
-        if par.dtype != torch.float16 or tuple(par.shape) != (pages, heads, page, d // c.group, 2) \
-                or not par.is_contiguous():
+        if par.dtype != torch.float16 or par.shape != pshape or not par.is_contiguous():
             raise ValueError("params must be contiguous fp16 [pages, heads, page_size, head_dim / group, 2] tensors")
     return _KV4(c.k_codes.data_ptr(), c.k_params.data_ptr(), c.v_codes.data_ptr(), c.v_params.data_ptr(), pages, page,
                 heads, d, int(c.group))
@@ -309,11 +331,11 @@ def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, table: torch.T
     _ints(cu, (count + 1,), "cu")
     _table(table, count)
     _status_ok(status)
-    with _launching(stream, cache.k_codes, cache.k_params, cache.v_codes, cache.v_params, k, v, table, cu, start,
+    with _Launching(stream, cache.k_codes, cache.k_params, cache.v_codes, cache.v_params, k, v, table, cu, start,
                     status) as s:
-        _check(lib().gptq_kv4_append(ctypes.byref(desc), _ptr(k), *_strides(k), _ptr(v), *_strides(v),
-                                     _DTYPE_CODE[k.dtype], k.shape[0], _ptr(table), table.shape[1], _ptr(cu),
-                                     _ptr(start), count, _ptr(status), s), "gptq_kv4_append")
+        _check(lib().gptq_kv4_append(ctypes.byref(desc), _at(k), *_strides(k), _at(v), *_strides(v),
+                                     _DTYPE_CODE[k.dtype], k.shape[0], _at(table), table.shape[1], _at(cu),
+                                     _at(start), count, _at(status), s), "gptq_kv4_append")
     return cache
 
 
@@ -333,12 +355,12 @@ def kv4_read(cache: KV4Cache, table: torch.Tensor, cu: torch.Tensor, tokens: int
         _ints(start, (count,), "start")
     _table(table, count)
     _status_ok(status)
-    with _launching(stream, cache.k_codes, cache.k_params, cache.v_codes, cache.v_params, table, cu, start,
+    with _Launching(stream, cache.k_codes, cache.k_params, cache.v_codes, cache.v_params, table, cu, start,
                     status) as s:
         k = torch.empty((int(tokens), desc.heads, desc.head_dim), dtype=dtype, device=cache.k_codes.device)
         v = torch.empty_like(k)
-        _check(lib().gptq_kv4_read(ctypes.byref(desc), _ptr(table), table.shape[1], _ptr(cu), _ptr(start), count,
-                                   int(tokens), _DTYPE_CODE[dtype], _ptr(k), _ptr(v), _ptr(status), s),
+        _check(lib().gptq_kv4_read(ctypes.byref(desc), _at(table), table.shape[1], _at(cu), _at(start), count,
+                                   int(tokens), _DTYPE_CODE[dtype], _at(k), _at(v), _at(status), s),
                "gptq_kv4_read")
     return k, v
 
@@ -364,20 +386,21 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, table: torch.Tensor, lengths
     _ints(lengths, (count,), "lengths")
     _table(table, count)
     _status_ok(status)
-    with _launching(stream, cache.k_codes, cache.k_params, cache.v_codes, cache.v_params, q, table, lengths, ws, out,
+    with _Launching(stream, cache.k_codes, cache.k_params, cache.v_codes, cache.v_params, q, table, lengths, ws, out,
                     status) as s:
         need = kv4_attention_workspace_size(count, hq, desc.heads, d, table.shape[1], desc.page_size)
         if ws is None or ws.numel() * ws.element_size() < need:
             ws = workspace(need, q.device)
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        _heads(out, q.dtype, "out")
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
-        _apart(out, q)
-        _check(lib().gptq_kv4_attention(ctypes.byref(desc), _ptr(q), *_strides(q), _DTYPE_CODE[q.dtype], count, hq,
-                                        _ptr(table), table.shape[1], _ptr(lengths),
-                                        float(d ** -0.5 if scale is None else scale), _ptr(out), *_strides(out),
-                                        _ptr(ws), ws.numel() * ws.element_size(), _ptr(status), s),
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        else:
+            _heads(out, q.dtype, "out")
+            if out.shape != q.shape:
+                raise ValueError("out must have q's shape")
+            _apart(out, q)
+        _check(lib().gptq_kv4_attention(ctypes.byref(desc), _at(q), *_strides(q), _DTYPE_CODE[q.dtype], count, hq,
+                                        _at(table), table.shape[1], _at(lengths),
+                                        float(d ** -0.5 if scale is None else scale), _at(out), *_strides(out),
+                                        _at(ws), ws.numel() * ws.element_size(), _at(status), s),
                "gptq_kv4_attention")
     return out
