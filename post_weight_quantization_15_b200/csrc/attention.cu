@@ -20,6 +20,13 @@
 //                    contiguous).  While one tile is in its softmax, the other's products run.
 // Every wait is bounded (GPTQ_ERR_TIMEOUT).
 //
+// Few queries over many keys leave SMs idle: then a cluster of 2, 4 or 8 blocks shares a pair
+// of tiles, each block taking a run of the key tiles; their (m, l, o) stay in shared memory,
+// and every block joins its share of the rows from all of them.  37 queries after 2011 keys,
+// 16 heads of 64: 39 us on one block per head, 16 on four; one query after 8000 keys, 8 heads
+// of 128: 148 us on one, 26 on eight; 2048 causal queries, 4 heads of 128: 45 us on one, 23 on
+// four.
+//
 // Rows that no query may see: scores of keys past a row's limit are replaced before they are
 // used; values past the sequence's end are zeroed in shared memory.  Inside a sequence a
 // causal tile still multiplies weights of 0 with values behind the diagonal, which is
@@ -41,6 +48,7 @@ namespace {
 
 constexpr int TQ = 128;                   // queries of a tile, keys of a tile
 constexpr int ATHREADS = 320;
+constexpr int SMS = 148;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float KEEP = 8.f;               // log2 of the largest weight under a kept maximum
 
@@ -61,6 +69,7 @@ struct AttnSmem {
   uint32_t tmem_base;
   int abort;
   int skip;
+  int valid;                              // this block's part of a shared pair of tiles is there
   int seq, tile;                          // this block's sequence and pair of tiles (-1: none)
 };
 
@@ -274,7 +283,98 @@ __device__ __noinline__ void seen_row(const AttentionArgs& A, int t, int h, int 
     if (e * 32 + lane < A.head_dim) store_from_float(o + e * 32 + lane, seen > 0 ? acc[e] / l : 0.f);
 }
 
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ void load_cluster(uint32_t addr, float (&v)[N]) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(addr) : "memory");
+  else
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "r"(addr) : "memory");
+}
+
+// Where a part's values lie in shared memory: row r's pieces of 4, in another order per row
+// (rows would share banks).
+template <int KD>
+__device__ __forceinline__ int part_at(int r, int piece) { return r * KD + ((piece ^ (r & (KD / 4 - 1))) << 2); }
+
+// Joins a share of the rows of a pair of tiles from the parts of the cluster's blocks: a warp
+// per row.
 template <int KD, typename T>
+__device__ __forceinline__ void join_parts(const AttentionArgs& A, AttnSmem<KD>& S, int h, int hk) {
+  constexpr int V = KD / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t size = cluster_size(), rank = tc::cluster_rank();
+  int ok = 1;                                             // lane c: block c's word, its (m, l)
+  if (lane < (int)size)
+    asm volatile("ld.shared::cluster.b32 %0, [%1];"
+                 : "=r"(ok) : "r"(tc::map_to_cta(tc::smem_u32(&S.valid), lane)) : "memory");
+  if (!__all_sync(0xffffffffu, ok)) return;
+  const int q0 = A.cu_q[S.seq], k0 = A.cu_k[S.seq];
+  const int lq = A.cu_q[S.seq + 1] - q0, lk = A.cu_k[S.seq + 1] - k0;
+  const int rows = min(2 * TQ, lq - S.tile * 2 * TQ);
+  for (int r = (int)rank + warp * (int)size; r < rows; r += (int)size * (ATHREADS / 32)) {
+    const int i = S.tile * 2 * TQ + r;                    // the query in its sequence
+    const int limit = max(0, min(lk, A.causal ? i + 1 + lk - lq : lk));
+    const uint32_t ml_at = tc::smem_u32(S.q[0]) + r * 8;
+    // feature piece: V consecutive values per lane
+    const uint32_t o_at = tc::smem_u32(S.kv[0]) + (part_at<KD>(r, lane * V / 4) + lane * V % 4) * 4;
+    float ml[2] = {-INFINITY, 0.f};
+    if (lane < (int)size) load_cluster(tc::map_to_cta(ml_at, lane), ml);
+    // a block that saw no key of this row has no values either
+    const unsigned live = __ballot_sync(0xffffffffu, !(ml[0] == -INFINITY && ml[1] == 0.f));
+    float o[8][V];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[c][e] = 0.f;
+      if (live >> c & 1) load_cluster(tc::map_to_cta(o_at, c), o[c]);
+    }
+    float top = ml[0];
+#pragma unroll
+    for (int i = 4; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i, 8));
+    const float f = exp2_approx(ml[0] - (top == -INFINITY ? 0.f : top));
+    float l = ml[1] * f, acc[V];
+#pragma unroll
+    for (int i = 4; i > 0; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i, 8);
+    l = __shfl_sync(0xffffffffu, l, 0);
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float w = __shfl_sync(0xffffffffu, f, c);
+      if (live >> c & 1) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = fmaf(o[c][e], w, acc[e]);
+      }
+    }
+    const float inv = 1.f / l;
+    bool nan = false;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      acc[e] = limit == 0 ? 0.f : acc[e] * inv;
+      nan |= acc[e] != acc[e];
+    }
+    T* dst = static_cast<T*>(A.o) + (int64_t)(q0 + i) * A.o_ts + h * A.o_hs;
+    if (lane * V < A.head_dim) {
+      uint32_t w[V / 2];
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) w[e] = pack2(acc[2 * e], acc[2 * e + 1], T());
+      if constexpr (V == 4) *reinterpret_cast<uint2*>(dst + lane * V) = make_uint2(w[0], w[1]);
+      else *reinterpret_cast<uint32_t*>(dst + lane * V) = w[0];
+    }
+    if (__any_sync(0xffffffffu, nan)) {
+      __syncwarp();                                       // the row's first values before its second
+      seen_row<T>(A, q0 + i, h, hk, k0, limit);
+    }
+  }
+}
+
+template <int KD, typename T, bool SPLIT>
 __global__ void __launch_bounds__(ATHREADS, 1)
 attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                  const __grid_constant__ CUtensorMap tv, const __grid_constant__ AttentionArgs A, int32_t* st) {
@@ -287,12 +387,14 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Smem& S = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = (int)blockIdx.x % A.heads_q, hk = h / (A.heads_q / A.heads_kv);
+  const int size = SPLIT ? (int)cluster_size() : 1, rank = SPLIT ? (int)tc::cluster_rank() : 0;
+  const int pair = (int)blockIdx.x / size;
+  const int h = pair % A.heads_q, hk = h / (A.heads_q / A.heads_kv);
 
   if (warp == 9) tc::tmem_alloc<512>(&S.tmem_base);
   if (warp == 0) {
     int seq, tile;
-    find_work(A, (int)blockIdx.x / A.heads_q, h == 0 ? st : nullptr, seq, tile);
+    find_work(A, pair / A.heads_q, h == 0 && rank == 0 ? st : nullptr, seq, tile);
     if (lane == 0) {
       S.seq = seq;
       S.tile = tile;
@@ -324,10 +426,17 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
   if (!S.skip) {
     const int q0 = A.cu_q[S.seq], k0 = A.cu_k[S.seq];
     const int lq = A.cu_q[S.seq + 1] - q0, lk = A.cu_k[S.seq + 1] - k0;
-    const Tile tl[2] = {make_tile(A, S.tile * 2 * TQ, lq, lk), make_tile(A, S.tile * 2 * TQ + TQ, lq, lk)};
+    Tile tl[2] = {make_tile(A, S.tile * 2 * TQ, lq, lk), make_tile(A, S.tile * 2 * TQ + TQ, lq, lk)};
+    int first = 0;                                        // this block's first key
+    if constexpr (SPLIT) {
+      const int share = (max(tl[0].blocks, tl[1].blocks) + size - 1) / size;
+      first = rank * share * TQ;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) tl[t].blocks = max(0, min(share, tl[t].blocks - rank * share));
+    }
     const int blocks = max(tl[0].blocks, tl[1].blocks);
     // the last tile of values reaches past the sequence's end: its rows there are zeroed
-    const int tail = blocks * TQ > lk ? lk - (blocks - 1) * TQ : 0;
+    const int tail = blocks > 0 && first + blocks * TQ > lk ? lk - first - (blocks - 1) * TQ : 0;
 
     if (warp == 8) {
       if (lane == 0) {
@@ -345,7 +454,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
           const CUtensorMap* map = (it & 1) ? &tv : &tk;
 #pragma unroll
           for (int c = 0; c < KD / 64; ++c)
-            tma_load_3d(S.kv[s] + c * (TQ * 128), map, &S.kv_full[s], c * 64, hk, k0 + (it >> 1) * TQ);
+            tma_load_3d(S.kv[s] + c * (TQ * 128), map, &S.kv_full[s], c * 64, hk, k0 + first + (it >> 1) * TQ);
 #pragma unroll
           for (int i = 0; i < NST; ++i) armed[i] += i == s;
         }
@@ -436,7 +545,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
 #pragma unroll
           for (int i = 0; i < TQ; ++i) s[i] *= c0;
         }
-        const int see = limit - j * TQ;
+        const int see = limit - first - j * TQ;
         if (__any_sync(0xffffffffu, see < TQ)) {
 #pragma unroll
           for (int i = 0; i < TQ; ++i) s[i] = i < see ? s[i] : -INFINITY;
@@ -494,7 +603,28 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&S.p_full[t]);
       }
-      if (ok && me.rows > 0) {
+      if constexpr (SPLIT) {
+        // both tiles' products are done with the shared memory that the parts go to
+        for (int u = 0; u < 2; ++u)
+          if (ok && tl[u].blocks > 0) ok = warp_wait(&S.o_full[u], 0, abort_flag);
+        if (ok) {
+          tc::tc_fence_after();
+          const int row = t * TQ + r;
+          reinterpret_cast<float2*>(S.q[0])[row] = make_float2(m * c, l);
+          float* part = reinterpret_cast<float*>(S.kv[0]);
+          if (me.blocks > 0) {
+#pragma unroll 1
+            for (int i = 0; i < KD; i += 32) {
+              float o[32];
+              tmem_ld32(to + i, o);
+              tmem_wait(o);
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<float4*>(part + part_at<KD>(row, (i + e) / 4)) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
+          }
+        }
+      } else if (ok && me.rows > 0) {
         if (me.blocks > 0) ok = warp_wait(&S.o_full[t], 0, abort_flag);
         if (ok) {
           tc::tc_fence_after();
@@ -526,6 +656,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             }
           }
           unsigned again = __ballot_sync(0xffffffffu, nan && mine);
+          __syncwarp();                                   // a row's first values before its second
           while (again != 0) {
             const int src = __ffs(again) - 1;
             again &= again - 1;
@@ -554,20 +685,56 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     __syncwarp();
     tc::tmem_dealloc<512>(taddr);
   }
+  if constexpr (SPLIT) {
+    if (threadIdx.x == 0) S.valid = !S.skip && !*abort_flag;
+    __syncwarp();
+    tc::cluster_sync();                                   // every block's part is there, or said not to be
+    join_parts<KD, T>(A, S, h, hk);
+    __syncwarp();
+    tc::cluster_sync();                                   // and has been read
+  }
+}
+
+// Blocks that share a pair of tiles: as many as run at once (74 clusters of two, 33 of four,
+// 15 of eight at this shared memory: a cluster stays in one part of the chip) and have two
+// key tiles or more of an average sequence.
+int cluster_of(const AttentionArgs& A) {
+  const int64_t work = (A.total_q / (2 * TQ) + (int64_t)A.count) * A.heads_q, tiles = A.total_k / A.count / TQ;
+  if (work <= 15 && tiles >= 16) return 8;
+  if (work <= 33 && tiles >= 8) return 4;
+  return work <= 74 && tiles >= 4 ? 2 : 1;
+}
+
+template <int KD, typename T, bool SPLIT>
+int launch(const AttentionArgs& A, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, int size,
+           int32_t* st, cudaStream_t s) {
+  const size_t smem = sizeof(AttnSmem<KD>) + 1024;
+  auto* kernel = attention_kernel<KD, T, SPLIT>;
+  GPTQ_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  // at most total_q / 256 + count pairs of tiles, of every head, and one block that reads every bound
+  const int64_t pairs = (A.total_q / (2 * TQ) + (int64_t)A.count) * A.heads_q + 1;
+  if (pairs * size > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(pairs * size));
+  cfg.blockDim = dim3(ATHREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)size;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = SPLIT ? 1 : 0;
+  GPTQ_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, A, st));
+  GPTQ_LAUNCH_CHECK();
+  return GPTQ_OK;
 }
 
 template <int KD, typename T>
-int launch(const AttentionArgs& A, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, int32_t* st,
-           cudaStream_t s) {
-  const size_t smem = sizeof(AttnSmem<KD>) + 1024;
-  auto* kernel = attention_kernel<KD, T>;
-  GPTQ_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  // at most total_q / 256 + count pairs of tiles, and one slot that reads every bound
-  const int64_t slots = A.total_q / (2 * TQ) + (int64_t)A.count + 1;
-  if (slots * A.heads_q > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
-  kernel<<<(unsigned)(slots * A.heads_q), ATHREADS, smem, s>>>(tq, tk, tv, A, st);
-  GPTQ_LAUNCH_CHECK();
-  return GPTQ_OK;
+int launch_any(const AttentionArgs& A, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, int32_t* st,
+               cudaStream_t s) {
+  const int size = cluster_of(A);
+  return size > 1 ? launch<KD, T, true>(A, tq, tk, tv, size, st, s) : launch<KD, T, false>(A, tq, tk, tv, 1, st, s);
 }
 
 // [tokens, heads, head_dim] in boxes of 128 tokens by 64 features; features past head_dim
@@ -593,8 +760,10 @@ int launch_attention(const AttentionArgs& A, int dtype, int32_t* st, cudaStream_
   }
   TraceScope ts("attention", "", 0.0, s);
   if (A.head_dim <= 64)
-    return dtype == GPTQ_F16 ? launch<64, __half>(A, tq, tk, tv, st, s) : launch<64, __nv_bfloat16>(A, tq, tk, tv, st, s);
-  return dtype == GPTQ_F16 ? launch<128, __half>(A, tq, tk, tv, st, s) : launch<128, __nv_bfloat16>(A, tq, tk, tv, st, s);
+    return dtype == GPTQ_F16 ? launch_any<64, __half>(A, tq, tk, tv, st, s)
+                             : launch_any<64, __nv_bfloat16>(A, tq, tk, tv, st, s);
+  return dtype == GPTQ_F16 ? launch_any<128, __half>(A, tq, tk, tv, st, s)
+                           : launch_any<128, __nv_bfloat16>(A, tq, tk, tv, st, s);
 }
 
 }  // namespace gptq

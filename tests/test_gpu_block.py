@@ -302,6 +302,39 @@ def test_attention_masked_rows_take_no_part(dt, d):
     assert torch.isinf(got[103:150, 2:, 5]).all() and torch.isfinite(got[103:150, 2:, :5]).all()
 
 
+# few queries over many keys: blocks that share a pair of query tiles
+SPLIT_CASES = [
+    ([1], [3000], 2, 1, 128, BF, True),
+    ([130], [2500], 3, 3, 64, HF, True),
+    ([257], [1800], 1, 1, 128, BF, False),
+    ([5, 0, 40], [4000, 0, 900], 2, 2, 64, BF, True),      # a sequence with far fewer keys than the average
+    ([1200], [-600], 1, 1, 128, HF, True),                 # the first queries see no key
+    ([3, 2], [1500, -2], 4, 4, 72, BF, True),              # a sequence without keys
+    ([300], [1749], 1, 1, 128, BF, True),                  # the last tile of keys reaches past the end by one
+]
+
+
+@pytest.mark.parametrize("lens,past,hq,hk,d,dt,causal", SPLIT_CASES)
+def test_attention_few_queries_over_many_keys(lens, past, hq, hk, d, dt, causal):
+    test_attention(lens, past, hq, hk, d, dt, causal)
+
+
+@pytest.mark.parametrize("dt,d", [(BF, 128), (HF, 64)])
+def test_attention_few_queries_masked_rows_take_no_part(dt, d):
+    """The same as above where several blocks share the keys."""
+    q, k, v, cq, ck = _attn_inputs([40], [2000], 4, 2, d, dt)
+    k2, v2 = k.clone(), v.clone()
+    v2[ck[-1]:] = float("nan")
+    k2[ck[-1]:] = float("inf")
+    v2[2020, 0] = float("nan")                               # queries 0 .. 19 do not see it
+    k2[2025, 1] = float("nan")
+    got = G.attention(q, k2, v2, _int(cq), _int(ck))
+    ref, tol = _attn_tol(_np(q), _np(k), _np(v), cq, ck, d ** -0.5, True, dt, U[dt])
+    _close(got[:20], ref[:20], tol[:20], "rows that see none")
+    _close(got[:25, 2:], ref[:25, 2:], tol[:25, 2:], "heads that see none")
+    assert torch.isnan(got[20:40, :2]).all() and torch.isnan(got[25:40, 2:]).all()
+
+
 def test_attention_large_scores_and_scale():
     """Scores in the thousands (weights 0 and 1), a negative and a zero scale."""
     q, k, v, cq, ck = _attn_inputs([140], [0], 2, 1, 128, HF)
