@@ -6,19 +6,22 @@
 // lo = min(x, 0), hi = max(x, 0) (-1 and 1 when equal), s = fp16((hi - lo) / 15) within
 // fp16's positive range, z = clamp(rint(-lo / s), 0, 15), code c = clamp(rint(x / s) + z,
 // 0, 15), value s (c - z).  x / s is a tie or at least 2^-17 relative away from one (x and s
-// have few bits), so its integer needs no IEEE division: with r = 1 / s the product q = x r
-// is within 2^-22 of it, and q + r (x - q s), the residual exact but for its own rounding,
-// lands on a tie's few bits exactly.  Adding 1.5 . 2^23 rounds to the nearest even integer
-// and leaves it in the low bits, where the eight codes of a word are summed under their
-// shifts (the constant's and the zero point's shares taken off once).
+// have few bits), so its integer needs no IEEE division: with r = 1 / s to 2^-23 the product
+// q = x r is within 2^-22 of it, and q + r (x - q s), the residual exact but for its own
+// rounding, lands on a tie's few bits exactly.  (hi - lo) / 15 is the rounded quotient by
+// Markstein's theorem: a residual and the rounded reciprocal (checked for all fp32
+// significands).  Adding 1.5 . 2^23 rounds to the nearest even integer and leaves it in the
+// low bits, where the eight codes of a word are summed under their shifts (the constant's
+// and the zero point's shares taken off once).
 //
-// Bound: HBM, with the issue slots close behind (about twelve instructions per value).  A
-// thread quantizes eight features (16 bytes in, one word of codes out); the group / 8
-// threads of a group find its range with shuffles, on packed 16-bit values.  A block takes
-// a few consecutive tokens, their places looked up once, and every thread reads its keys
-// and values of two tokens before it uses the first.  (One token per block, IEEE divisions and
-// integer conversions took 366 us for 15,625 tokens of 32 heads x 128 written and read back
-// where these take 203.)
+// Bound: HBM, with the issue slots close behind.  A thread quantizes sixteen features of a
+// group, eight in each of its halves (two 16-byte loads side by side across the group's
+// group / 16 threads, two words of codes), of keys and values; the group's range is found with
+// shuffles on packed 16-bit values.  A block takes a few consecutive tokens, their places
+// looked up once.  (15,625 tokens of 32 heads x 128 in bf16, written and read back: 369 us with
+// one token per block, IEEE divisions and integer conversions; 203 with eight features per
+// thread, 134 of it the writing; now 148, 87 of it the writing, whose 65 million warp
+// instructions take 74% of the issue slots.)
 #include <type_traits>
 
 #include "common.cuh"
@@ -56,12 +59,12 @@ __device__ __forceinline__ void find_rows(const KV4Cache& C, const int32_t* tabl
   __syncthreads();
 }
 
-// A thread's place: unit u (of heads . words) of every subs-th token, or units u, u + 256, ...
-// of every token.
+// A thread's place among a token's `per` units: unit u0 of every subs-th token, or units u0,
+// u0 + 256, ... of every token.
 struct Units {
   int per, sub, subs, u0;
-  __device__ __forceinline__ Units(const KV4Cache& C) {
-    per = C.heads * (C.head_dim / 8);
+  __device__ __forceinline__ explicit Units(int units) {
+    per = units;
     subs = max(1, THREADS / per);
     sub = (int)threadIdx.x / per;                     // subs: no token
     u0 = per < THREADS ? (int)threadIdx.x % per : (int)threadIdx.x;
@@ -89,41 +92,64 @@ __device__ __forceinline__ float2 wide2(uint32_t w, __nv_bfloat16) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// Eight values of a group (`lanes` threads share it) -> their word of codes, and the group's
-// scale and zero point; `bad` if the group holds a NaN or an infinity.  Whole warp.
+__device__ __forceinline__ float reciprocal(float x) {     // to 2^-23
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Sixteen values of a group that `lanes` threads share -> their two words, and the group's scale
+// and zero point; `bad` if the group holds a NaN or an infinity.  Whole warp.
 template <typename T>
-__device__ __forceinline__ uint32_t quantize8(const uint4& raw, int lanes, __half2& par, bool& bad) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+__device__ __forceinline__ void quantize16(const uint4 (&raw)[2], int lanes, uint32_t (&word)[2], __half2& par,
+                                           bool& bad) {
+  const uint32_t w[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
   // (-smallest, largest) as one pair, 0 included
-  const uint32_t lo = min2(min2(w[0], w[1], T()), min2(w[2], w[3], T()), T());
-  const uint32_t hi = max2(max2(w[0], w[1], T()), max2(w[2], w[3], T()), T());
+  uint32_t lo = w[0], hi = w[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    lo = min2(lo, w[i], T());
+    hi = max2(hi, w[i], T());
+  }
   const uint32_t neg = lo ^ 0x80008000u;
   uint32_t ends = max2(__byte_perm(neg, hi, 0x5410), __byte_perm(neg, hi, 0x7632), T());
   ends = max2(ends, 0u, T());
   for (int o = 1; o < lanes; o <<= 1) ends = max2(ends, __shfl_xor_sync(0xffffffffu, ends, o), T());
   float2 e = wide2(ends, T());
-  bad = !(fmaxf(e.x, e.y) < INFINITY) || e.x != e.x || e.y != e.y;
+  bad = !(e.x < INFINITY) || !(e.y < INFINITY);
   if (e.x == 0.f && e.y == 0.f) e = make_float2(1.f, 1.f);
-  const __half s16 = __float2half_rn(fminf(fmaxf(__fdiv_rn(e.y + e.x, 15.f), 5.9604644775390625e-08f), 65504.f));
-  const float s = __half2float(s16), r = 1.f / s;
-  const float z = fminf(rintf(__fdiv_rn(e.x, s)), 15.f);
-  const float most = 15.f - z;
+  constexpr float FIFTEENTH = 1.f / 15.f;
+  const float range = e.y + e.x;
+  float scale = range * FIFTEENTH;
+  scale = fmaf(fmaf(scale, -15.f, range), FIFTEENTH, scale);
+  if (!(range < INFINITY)) scale = range;                 // (two bf16 ends beyond fp32 together)
+  const __half s16 = __float2half_rn(fminf(fmaxf(scale, 5.9604644775390625e-08f), 65504.f));
+  const float s = __half2float(s16), r = reciprocal(s);
   constexpr float ROUND = 12582912.f;     // 1.5 . 2^23
-  uint32_t word = ((uint32_t)(int)z - __float_as_uint(ROUND)) * 0x11111111u;
+  float z = e.x * r;
+  z = fminf(fmaf(r, fmaf(-z, s, e.x), z), 15.f) + ROUND;
+  const uint32_t zi = __float_as_uint(z) - __float_as_uint(ROUND);
+  z -= ROUND;
+  const float most = 15.f - z;
+  const uint32_t offset = (zi - __float_as_uint(ROUND)) * 0x11111111u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 x = wide2(w[i], T());
-    const float v[2] = {x.x, x.y};
+  for (int h = 0; h < 2; ++h) {
+    uint32_t sum = offset;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      float q = v[k] * r;
-      q = fmaf(r, fmaf(-q, s, v[k]), q);
-      q = fminf(fmaxf(q, -z), most) + ROUND;
-      word += __float_as_uint(q) << (8 * i + 4 * k);
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = wide2(w[4 * h + i], T());
+      const float v[2] = {x.x, x.y};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float q = v[k] * r;
+        q = fmaf(r, fmaf(-q, s, v[k]), q);
+        q = fminf(fmaxf(q, -z), most) + ROUND;
+        sum += __float_as_uint(q) << (8 * i + 4 * k);
+      }
     }
+    word[h] = sum;
   }
   par = __halves2half2(s16, __float2half_rn(z));
-  return word;
 }
 
 template <typename T>
@@ -135,45 +161,45 @@ __global__ void __launch_bounds__(THREADS) kv4_append_kernel(const __grid_consta
   if (has_error(st)) return;
   const int t0 = (int)blockIdx.x * per_block, n = min(per_block, tokens - t0);
   find_rows(C, table, width, cu, start, count, t0, n, rows, st);
-  const Units U(C);
-  const int words = C.head_dim / 8, lanes = C.group / 8, groups = C.head_dim / C.group;
-  const int lw = __ffs(words) - 1, ll = __ffs(lanes) - 1;
+  const Units U(C.heads * (C.head_dim / 16));
+  const int words = C.head_dim / 8, lanes = C.group / 16, groups = C.head_dim / C.group;
+  const int lw = __ffs(words / 2) - 1, ll = __ffs(lanes) - 1;
   // every thread goes through every step: the shuffles take whole warps
   for (int step = 0; step < U.per; step += THREADS) {
-    const int u = U.u0 + step, head = u >> lw, w = u & (words - 1);
-    for (int i0 = 0; i0 < n; i0 += 2 * U.subs) {
+    const int u = U.u0 + step, head = u >> lw, in_head = u & (words / 2 - 1);
+    const int group = in_head >> ll, lane = in_head & (lanes - 1), w = 2 * (group << ll) + lane;   // words w, w + lanes
+    for (int i0 = 0; i0 < n; i0 += U.subs) {
+      const int i = i0 + U.sub;
+      const int64_t row = u < U.per && U.sub < U.subs && i < n ? rows[i] : -1;
       uint4 raw[2][2];
-      int64_t row[2];
 #pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        const int i = i0 + a * U.subs + U.sub;
-        row[a] = u < U.per && U.sub < U.subs && i < n ? rows[i] : -1;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          raw[a][kv] = make_uint4(0, 0, 0, 0);
-          if (row[a] >= 0)
-            raw[a][kv] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(in.p[kv]) +
-                                                               (int64_t)(t0 + i) * in.token_stride[kv] +
-                                                               head * in.head_stride[kv] + w * 8));
+      for (int kv = 0; kv < 2; ++kv) {
+        raw[kv][0] = raw[kv][1] = make_uint4(0, 0, 0, 0);
+        if (row >= 0) {
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(in.p[kv]) +
+                                                            (int64_t)(t0 + i) * in.token_stride[kv] +
+                                                            head * in.head_stride[kv]) + w;
+          raw[kv][0] = __ldcs(src);
+          raw[kv][1] = __ldcs(src + lanes);
         }
       }
 #pragma unroll
-      for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          __half2 par;
-          bool bad;
-          uint32_t word = quantize8<T>(raw[a][kv], lanes, par, bad);
-          if (row[a] < 0) continue;
-          if (bad) {                      // the whole group reads back as NaN
-            word = 0;
-            par = __halves2half2(__ushort_as_half((unsigned short)0x7fffu), __ushort_as_half((unsigned short)0));
-            if ((w & (lanes - 1)) == 0) set_error(st, GPTQ_ERR_NONFINITE, t0 + i0 + a * U.subs + U.sub, STAGE_KV4);
-          }
-          const int64_t at = row[a] + (int64_t)head * C.page_size;
-          C.codes[kv][at * words + w] = (int32_t)word;
-          if ((w & (lanes - 1)) == 0) reinterpret_cast<__half2*>(C.params[kv])[at * groups + (w >> ll)] = par;
+      for (int kv = 0; kv < 2; ++kv) {
+        __half2 par;
+        uint32_t word[2];
+        bool bad;
+        quantize16<T>(raw[kv], lanes, word, par, bad);
+        if (row < 0) continue;
+        if (bad) {                        // the whole group reads back as NaN
+          word[0] = word[1] = 0;
+          par = __halves2half2(__ushort_as_half((unsigned short)0x7fffu), __ushort_as_half((unsigned short)0));
+          if (lane == 0) set_error(st, GPTQ_ERR_NONFINITE, t0 + i, STAGE_KV4);
         }
+        const int64_t at = row + (int64_t)head * C.page_size;
+        C.codes[kv][at * words + w] = (int32_t)word[0];
+        C.codes[kv][at * words + w + lanes] = (int32_t)word[1];
+        if (lane == 0) reinterpret_cast<__half2*>(C.params[kv])[at * groups + group] = par;
+      }
     }
   }
 }
@@ -187,27 +213,38 @@ __global__ void __launch_bounds__(THREADS) kv4_read_kernel(const __grid_constant
   if (has_error(st)) return;
   const int t0 = (int)blockIdx.x * per_block, n = min(per_block, tokens - t0);
   find_rows(C, table, width, cu, start, count, t0, n, rows, st);
-  const Units U(C);
+  const Units U(C.heads * (C.head_dim / 16));
   if (U.sub >= U.subs) return;
-  const int words = C.head_dim / 8, lanes = C.group / 8, groups = C.head_dim / C.group;
-  const int lw = __ffs(words) - 1, ll = __ffs(lanes) - 1;
+  const int words = C.head_dim / 8, lanes = C.group / 16, groups = C.head_dim / C.group;
+  const int lw = __ffs(words / 2) - 1, ll = __ffs(lanes) - 1;
   for (int u = U.u0; u < U.per; u += THREADS) {
-    const int head = u >> lw, w = u & (words - 1);
+    const int head = u >> lw, in_head = u & (words / 2 - 1);
+    const int group = in_head >> ll, w = 2 * (group << ll) + (in_head & (lanes - 1));      // words w, w + lanes
 #pragma unroll 2
     for (int i = U.sub; i < n; i += U.subs) {
       const int64_t row = rows[i];
       if (row < 0) continue;
       const int64_t at = row + (int64_t)head * C.page_size;
+      uint32_t word[2][2];
+      __half2 par[2];
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        const uint32_t word = (uint32_t)C.codes[kv][at * words + w];
-        const __half2 par = reinterpret_cast<const __half2*>(C.params[kv])[at * groups + (w >> ll)];
-        // 2^23 + code is the code in the low bits of 2^23's pattern; less 2^23 + z it is code - z, exactly
-        const float s = __low2float(par), z = 8388608.f + __high2float(par);
-        float x[8];
+        word[kv][0] = (uint32_t)C.codes[kv][at * words + w];
+        word[kv][1] = (uint32_t)C.codes[kv][at * words + w + lanes];
+        par[kv] = reinterpret_cast<const __half2*>(C.params[kv])[at * groups + group];
+      }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = s * (__uint_as_float(0x4B000000u | ((word >> (4 * e)) & 15u)) - z);
-        store8((kv ? v : k) + ((int64_t)(t0 + i) * C.heads + head) * C.head_dim + w * 8, x);
+      for (int kv = 0; kv < 2; ++kv) {
+        // 2^23 + code is the code in the low bits of 2^23's pattern; less 2^23 + z it is code - z, exactly
+        const float s = __low2float(par[kv]), z = 8388608.f + __high2float(par[kv]);
+        T* dst = (kv ? v : k) + ((int64_t)(t0 + i) * C.heads + head) * C.head_dim + w * 8;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = s * (__uint_as_float(0x4B000000u | ((word[kv][h] >> (4 * e)) & 15u)) - z);
+          store8(dst + h * lanes * 8, x);
+        }
       }
     }
   }
@@ -215,7 +252,7 @@ __global__ void __launch_bounds__(THREADS) kv4_read_kernel(const __grid_constant
 
 // Tokens of a block: as many as keep its threads busy, more while there are blocks to spare.
 int tokens_per_block(const KV4Cache& C, int tokens) {
-  const int per = C.heads * (C.head_dim / 8);
+  const int per = C.heads * (C.head_dim / 16);
   int n = per < THREADS ? THREADS / per : 1;
   if (n > MOST) n = MOST;
   while (n * 2 <= MOST && n * (int64_t)per < 8 * THREADS && cdiv(tokens, n * 2) >= ENOUGH) n *= 2;
