@@ -14,10 +14,14 @@
 // 32 above) and every statistic is taken there; x, y and the gate are read and xn and h
 // written once; the parameters come from L1 and are applied a row piece at a time, so that
 // x and y are all that a thread holds.  Rows of up to 512 values take one warp each (no
-// block barrier), longer rows one block.  Where a row does not start on a 16-byte boundary
-// (an odd d or stride) the threads read single values side by side instead of eight each,
-// with their number a power of two known when compiled, so that a value costs no address
-// arithmetic.
+// block barrier), longer rows one block.  Where rows do not start on 16-byte boundaries (an
+// odd d or stride) a thread of a 16-bit stream still takes eight consecutive values: it reads
+// the aligned 16-byte pieces that hold them and shifts, and writes by way of shared memory,
+// where each thread picks up what belongs to one aligned piece; single values only at a row's
+// ends.  (fp32 streams read single values side by side.)  32768 rows of 4096, bf16 with fp32
+// Y: 203 us, 1.01 of the measured copy bandwidth.  2039 rows of 5125, fp16, norms on both
+// sides: 117 us with everything in registers that spilled, 65 with single values, 57 shifted, 51
+// with three blocks per SM; about 1400 instructions per warp and row bound it.
 #include "common.cuh"
 #include "internal.h"
 #include "vec_io.cuh"
@@ -43,13 +47,16 @@ struct NormArgs {
   int center;
 };
 
+constexpr int ANY = -1;
+
 // A row's threads and their places.  T = 0: any number of threads with eight consecutive
-// values per piece; else T threads with single values side by side.
+// values per piece, which lie on 16-byte boundaries; ANY: the same on any boundaries; else T
+// threads with single values side by side.
 template <int T>
 struct Row {
-  __device__ static __forceinline__ int threads() { return T ? T : (int)blockDim.x; }
+  __device__ static __forceinline__ int threads() { return T > 0 ? T : (int)blockDim.x; }
   __device__ static __forceinline__ int at(int v, int e) {
-    return T == 0 ? (v * (int)blockDim.x + (int)threadIdx.x) * 8 + e : (v * 8 + e) * T + (int)threadIdx.x;
+    return T <= 0 ? (v * (int)blockDim.x + (int)threadIdx.x) * 8 + e : (v * 8 + e) * T + (int)threadIdx.x;
   }
 };
 
@@ -68,6 +75,58 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
   return v;
 }
 
+// w[i] <- the word that starts `by` bytes (even, below 16) after w[i], i < N.
+template <int N>
+__device__ __forceinline__ void shift(uint32_t (&w)[N + 4], uint32_t by) {
+  if (by & 8) {
+#pragma unroll
+    for (int i = 0; i < N + 2; ++i) w[i] = w[i + 2];
+  }
+  if (by & 4) {
+#pragma unroll
+    for (int i = 0; i < N + 1; ++i) w[i] = w[i + 1];
+  }
+  if (by & 2) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  }
+}
+
+// Eight values from e0 (a multiple of 8) of a row on any boundary.  Only aligned pieces that
+// hold a value of the row are read.
+template <typename S>
+__device__ __forceinline__ void load8_any(const S* row, int d, int e0, float (&x)[8]) {
+  constexpr int N = sizeof(S) * 2;        // words of eight values
+  const uint32_t mis = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
+  const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(row) - mis) + e0 / 8 * (N / 4);
+  const int left = (d - e0) * (int)sizeof(S) + (int)mis;  // bytes of the row from p on
+  uint32_t w[N + 4];
+#pragma unroll
+  for (int i = 0; i < N / 4 + 1; ++i) {
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (left > 16 * i && (i < N / 4 || mis != 0)) u = p[i];
+    w[4 * i] = u.x;
+    w[4 * i + 1] = u.y;
+    w[4 * i + 2] = u.z;
+    w[4 * i + 3] = u.w;
+  }
+  if (mis != 0) shift<N>(w, mis);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(S) == 4) {
+      x[2 * i] = __uint_as_float(w[2 * i]);
+      x[2 * i + 1] = __uint_as_float(w[2 * i + 1]);
+    } else {
+      unpack2(w[i], x[2 * i], x[2 * i + 1], S());
+    }
+  }
+  if (e0 + 8 > d) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e0 + e >= d) x[e] = 0.f;
+  }
+}
+
 // Piece v (eight values) of a row; values past d read as 0.
 template <int T, typename S>
 __device__ __forceinline__ void load_piece(const S* row, int d, int v, float (&x)[8]) {
@@ -75,6 +134,8 @@ __device__ __forceinline__ void load_piece(const S* row, int d, int v, float (&x
   for (int e = 0; e < 8; ++e) x[e] = 0.f;
   if constexpr (T == 0) {
     if (Row<T>::at(v, 0) < d) load8(row + Row<T>::at(v, 0), x);
+  } else if constexpr (T == ANY) {
+    load8_any(row, d, Row<T>::at(v, 0), x);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -115,8 +176,49 @@ __device__ __forceinline__ void apply(const void* p, int64_t off, int dtype, int
   });
 }
 
+// A row of 16-bit values to any boundary, by way of `buf` (16 bytes for each eight values).
+template <int V, typename S>
+__device__ __forceinline__ void store_any(S* row, int d, const float (&x)[V * 8], uint4* buf) {
+  const int n = (int)blockDim.x, pieces = (d + 7) / 8;
+  if (n == 32) __syncwarp();              // the last row's readers are done
+  else __syncthreads();
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const float* y = &x[v * 8];
+    const int i = v * n + (int)threadIdx.x;
+    if (i < pieces) buf[i] = make_uint4(pack2(y[0], y[1], S()), pack2(y[2], y[3], S()), pack2(y[4], y[5], S()), pack2(y[6], y[7], S()));
+  }
+  if (n == 32) __syncwarp();
+  else __syncthreads();
+  const uint32_t mis = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
+  const int off = (int)mis / 2;           // piece c of memory: values 8 c - off .. 8 c - off + 7
+  for (int c = (int)threadIdx.x; c * 8 - off < d; c += n) {
+    const uint4 a = c > 0 ? buf[c - 1] : make_uint4(0, 0, 0, 0);
+    const uint4 b = c < pieces ? buf[c] : make_uint4(0, 0, 0, 0);
+    uint32_t w[8] = {b.x, b.y, b.z, b.w, 0, 0, 0, 0};
+    if (mis != 0) {
+      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+      w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+      shift<4>(w, 16 - mis);
+    }
+    const int e0 = c * 8 - off;
+    if (e0 >= 0 && e0 + 8 <= d) {
+      *reinterpret_cast<uint4*>(row + e0) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e0 + e >= 0 && e0 + e < d)
+          reinterpret_cast<uint16_t*>(row)[e0 + e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+    }
+  }
+}
+
 template <int V, int T, typename S>
-__device__ __forceinline__ void store_row(S* row, int d, const float (&x)[V * 8]) {
+__device__ __forceinline__ void store_row(S* row, int d, const float (&x)[V * 8], uint4* buf) {
+  if constexpr (T == ANY) {
+    if constexpr (sizeof(S) == 2) store_any<V>(row, d, x, buf);
+    return;
+  }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     if constexpr (T == 0) {
@@ -143,7 +245,7 @@ __device__ __forceinline__ void norm_row(float (&x)[V * 8], const void* w, const
     for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        x[v * 8 + e] = Row<T>::at(v, T ? e : 0) < A.d ? x[v * 8 + e] - mean : 0.f;
+        x[v * 8 + e] = Row<T>::at(v, T == 0 ? 0 : e) < A.d ? x[v * 8 + e] - mean : 0.f;
   }
   float q = 0.f;
 #pragma unroll
@@ -153,11 +255,14 @@ __device__ __forceinline__ void norm_row(float (&x)[V * 8], const void* w, const
   if (b != nullptr) apply<V, T>(b, 0, A.p_dtype, A.d, x, [](float a, float p) { return a + p; });
 }
 
-// ROWS rows of a warp each (T 0 or 32), or one row per block.
-template <typename TX, int V, int T, int ROWS>
-__global__ void __launch_bounds__(ROWS > 1 ? 32 * ROWS : (T ? T : 1024), 1024 / (ROWS > 1 ? 32 * ROWS : (T ? T : 1024)))
+// ROWS rows of a warp each (T 0, ANY or 32), or one row per block of up to MAXT threads (384:
+// three blocks to an SM, which hide each other's barriers; four would spill).
+template <typename TX, int V, int T, int ROWS, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 384 ? 3 : 1024 / MAXT)
 add_norm_kernel(const NormArgs A, const int32_t* st) {
   __shared__ float part[4][32];
+  extern __shared__ uint4 pieces[];       // ANY: 16 bytes for each eight values of the block's rows
+  uint4* buf = pieces + (int)threadIdx.y * 64;
   if (has_error(st)) return;
   const int row = (int)blockIdx.x * ROWS + (int)threadIdx.y;
   if (ROWS > 1 && row >= A.tokens) return;
@@ -175,10 +280,10 @@ add_norm_kernel(const NormArgs A, const int32_t* st) {
     if constexpr (V != 2) load_row<V, T>(X, A.d, x);
 #pragma unroll
     for (int i = 0; i < V * 8; ++i) y[i] = round_to<TX>(fmaf(A.alpha, y[i], x[i]));
-    store_row<V, T>(static_cast<TX*>(A.Xn) + (int64_t)row * A.ld_xn, A.d, y);
+    store_row<V, T>(static_cast<TX*>(A.Xn) + (int64_t)row * A.ld_xn, A.d, y, buf);
   }
   norm_row<V, T>(y, A.weight, A.bias, A, part + 2);
-  store_row<V, T>(static_cast<TX*>(A.h) + (int64_t)row * A.ld_h, A.d, y);
+  store_row<V, T>(static_cast<TX*>(A.h) + (int64_t)row * A.ld_h, A.d, y, buf);
 }
 
 template <typename TX>
@@ -187,17 +292,29 @@ void launch(const NormArgs& A, bool vec, const int32_t* st, cudaStream_t s) {
   const dim3 warps(32, 8);
   if (vec) {
     const unsigned thr = (unsigned)(cdiv(cdiv(A.d, A.d <= 16384 ? 16 : 32), 32) * 32);
-    if (A.d <= 512) add_norm_kernel<TX, 2, 0, 8><<<rows8, warps, 0, s>>>(A, st);
-    else if (A.d <= 16384) add_norm_kernel<TX, 2, 0, 1><<<rows, thr, 0, s>>>(A, st);
-    else add_norm_kernel<TX, 4, 0, 1><<<rows, thr, 0, s>>>(A, st);
+    if (A.d <= 512) add_norm_kernel<TX, 2, 0, 8, 256><<<rows8, warps, 0, s>>>(A, st);
+    else if (A.d <= 16384) add_norm_kernel<TX, 2, 0, 1, 1024><<<rows, thr, 0, s>>>(A, st);
+    else add_norm_kernel<TX, 4, 0, 1, 1024><<<rows, thr, 0, s>>>(A, st);
+    return;
+  }
+  if constexpr (sizeof(TX) == 2) {
+    if (A.d <= 512) add_norm_kernel<TX, 2, ANY, 8, 256><<<rows8, warps, 8 * 64 * 16, s>>>(A, st);
+    else if (A.d <= 16384) {
+      const unsigned thr = (unsigned)(cdiv(cdiv(A.d, 16), 32) * 32);
+      const size_t smem = (size_t)cdiv(A.d, 8) * 16;
+      if (thr <= 384) add_norm_kernel<TX, 2, ANY, 1, 384><<<rows, thr, smem, s>>>(A, st);
+      else add_norm_kernel<TX, 2, ANY, 1, 1024><<<rows, thr, smem, s>>>(A, st);
+    } else {
+      add_norm_kernel<TX, 4, 1024, 1, 1024><<<rows, 1024, 0, s>>>(A, st);
+    }
   } else {
-    if (A.d <= 512) add_norm_kernel<TX, 2, 32, 8><<<rows8, warps, 0, s>>>(A, st);
-    else if (A.d <= 1024) add_norm_kernel<TX, 2, 64, 1><<<rows, 64, 0, s>>>(A, st);
-    else if (A.d <= 2048) add_norm_kernel<TX, 2, 128, 1><<<rows, 128, 0, s>>>(A, st);
-    else if (A.d <= 4096) add_norm_kernel<TX, 2, 256, 1><<<rows, 256, 0, s>>>(A, st);
-    else if (A.d <= 8192) add_norm_kernel<TX, 2, 512, 1><<<rows, 512, 0, s>>>(A, st);
-    else if (A.d <= 16384) add_norm_kernel<TX, 2, 1024, 1><<<rows, 1024, 0, s>>>(A, st);
-    else add_norm_kernel<TX, 4, 1024, 1><<<rows, 1024, 0, s>>>(A, st);
+    if (A.d <= 512) add_norm_kernel<TX, 2, 32, 8, 256><<<rows8, warps, 0, s>>>(A, st);
+    else if (A.d <= 1024) add_norm_kernel<TX, 2, 64, 1, 64><<<rows, 64, 0, s>>>(A, st);
+    else if (A.d <= 2048) add_norm_kernel<TX, 2, 128, 1, 128><<<rows, 128, 0, s>>>(A, st);
+    else if (A.d <= 4096) add_norm_kernel<TX, 2, 256, 1, 256><<<rows, 256, 0, s>>>(A, st);
+    else if (A.d <= 8192) add_norm_kernel<TX, 2, 512, 1, 512><<<rows, 512, 0, s>>>(A, st);
+    else if (A.d <= 16384) add_norm_kernel<TX, 2, 1024, 1, 1024><<<rows, 1024, 0, s>>>(A, st);
+    else add_norm_kernel<TX, 4, 1024, 1, 1024><<<rows, 1024, 0, s>>>(A, st);
   }
 }
 
