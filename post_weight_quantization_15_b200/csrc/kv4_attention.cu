@@ -34,6 +34,7 @@
 #include <math.h>
 
 #include <climits>
+#include <cstdint>
 
 #include "common.cuh"
 #include "internal.h"
@@ -122,8 +123,9 @@ struct Finder {
       if (here) {
         const int64_t r = rel - (end - slots_of(n, heads));
         p.b = b0 + lo;
-        p.hx = (int)(r / (n + 1));
-        p.t = (int)(r % (n + 1));
+        // (a quotient in 32 bits wherever it can be one)
+        p.hx = r <= UINT32_MAX ? (int)((uint32_t)r / (uint32_t)(n + 1)) : (int)(r / (n + 1));
+        p.t = (int)(r - (int64_t)p.hx * (n + 1));
         p.tiles = n;
         open = false;
       }
@@ -189,13 +191,29 @@ struct Zero {
 __device__ __forceinline__ Zero make_zero(__half2 z) {
   return Zero{__hneg2(__hadd2(z, __floats2half2_rn(1024.f, 1024.f))), __hneg2(__hadd2(z, __floats2half2_rn(64.f, 64.f)))};
 }
-__device__ __forceinline__ uint32_t code_lo(uint32_t x, const Zero& z) {
-  const uint32_t v = (x & 0x000F000Fu) | 0x64006400u;
+// (x & mask) | 1024's pattern in both halves, in one instruction: with both constants visible
+// it is split into two, and the ALU is what bounds this kernel.
+__device__ __forceinline__ uint32_t mantissas(uint32_t x, uint32_t mask) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(mask), "r"(0x64006400u));
+  return r;
+}
+struct Masks {
+  uint32_t lo, hi;
+};
+__device__ __forceinline__ Masks make_masks() {
+  Masks m;
+  asm volatile("mov.b32 %0, 0x000F000F;" : "=r"(m.lo));
+  asm volatile("mov.b32 %0, 0x00F000F0;" : "=r"(m.hi));
+  return m;
+}
+__device__ __forceinline__ uint32_t code_lo(uint32_t x, const Masks& m, const Zero& z) {
+  const uint32_t v = mantissas(x, m.lo);
   const __half2 h = __hadd2(*reinterpret_cast<const __half2*>(&v), z.lo);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ uint32_t code_hi(uint32_t x, const Zero& z) {
-  const uint32_t v = (x & 0x00F000F0u) | 0x64006400u;
+__device__ __forceinline__ uint32_t code_hi(uint32_t x, const Masks& m, const Zero& z) {
+  const uint32_t v = mantissas(x, m.hi);
   const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&v), __floats2half2_rn(0.0625f, 0.0625f), z.hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
@@ -271,14 +289,17 @@ kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
   __syncthreads();
   const int runs = runs_of(all), run = (int)blockIdx.x * WARPS + warp;
   if (S.skip || all == 0 || run - warp >= runs) return;
-  const int64_t begin = run < runs ? run_begin(all, runs, run) : 0;
-  const int mine = run < runs ? (int)(run_begin(all, runs, run + 1) - begin) : 0;
+  // run_begin(all, runs, run), with one long division
+  const int64_t each = all <= UINT32_MAX ? (int64_t)((uint32_t)all / (uint32_t)runs) : all / runs;
+  const int over = (int)(all - each * runs), b0 = over * run / runs, b1 = over * (run + 1) / runs;   // RUNS^2 < 2^31
+  const int64_t begin = each * run + b0;
+  const int mine = run < runs ? (int)(each + b1 - b0) : 0;
 
   // lane i holds what slot (made & ~31) + i needs
   Finder finder;
   const int box = min(A.C.page_size, TT), parts = TT / box;      // tokens of a tile in one page; pages of a tile
   int made = 0;
-  int64_t row0 = 0, row1 = 0;
+  uint32_t row0 = 0, row1 = 0;            // (more than 2^32 rows do not fit the device)
   int4 d0 = make_int4(0, 0, 0, 0);
   auto produce = [&]() {
     if (made < mine) {
@@ -306,7 +327,7 @@ kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
             } else if (parts == 1) {
               page = -1;                  // the same page as the first half
             }
-            const int64_t row = kv4_row(A.C, page, head, pos & (A.C.page_size - 1));
+            const uint32_t row = (uint32_t)kv4_row(A.C, page, head, pos & (A.C.page_size - 1));
             if (k == 0) row0 = row;
             else row1 = page < 0 ? row0 + 16 : row;
           }
@@ -314,7 +335,7 @@ kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
         }
       }
       const int src = made & 31, s = made % STAGES;
-      const int64_t r[2] = {__shfl_sync(0xffffffffu, row0, src), __shfl_sync(0xffffffffu, row1, src)};
+      const uint32_t r[2] = {__shfl_sync(0xffffffffu, row0, src), __shfl_sync(0xffffffffu, row1, src)};
       if (lane == src) S.desc[warp][s] = d0;
       if (__shfl_sync(0xffffffffu, d0.z, src) >= 0) {
         auto& stage = S.ring[warp][s];
@@ -327,12 +348,12 @@ kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
           for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int i = 0; i < P16 / 32; ++i)    // 32 pieces on, the rows' swizzle repeats
-              copy16(dst + (k * P16 + i * 32) * 16, base + r[k] * (D / 2) + i * 512);
+              copy16(dst + (k * P16 + i * 32) * 16, base + (uint64_t)r[k] * (D / 2) + i * 512);
           constexpr int Q16 = 4 * NG;       // pieces of 16 tokens' scales and zero points
           if (lane < 2 * Q16) {
             const int k = lane / Q16;
             copy16(smem_addr(stage.params[kv]) + lane * 16,
-                   reinterpret_cast<const char*>(A.C.params[kv]) + (k ? r[1] : r[0]) * (NG * 4) + (lane % Q16) * 16);
+                   reinterpret_cast<const char*>(A.C.params[kv]) + (uint64_t)(k ? r[1] : r[0]) * (NG * 4) + (lane % Q16) * 16);
           }
         }
       }
@@ -344,6 +365,7 @@ kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
   for (int i = 0; i < STAGES; ++i) produce();
   __syncwarp();
 
+  const Masks masks = make_masks();
   // the state of the head set at hand: heads 2 j and 2 j + 1 of it
   float acc[MT][4], m[2], l[2];
   int ve[NG];                             // weights of group i carry 2^(10 - ve[i])
@@ -389,12 +411,16 @@ kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
       float f = ldexpf(fabsf(A.scale) * LOG2E, e2 - 11);
       const float sign = f == 0.f ? 0.f : (A.scale < 0.f ? -1.f : 1.f);
       f = f == 0.f ? 1.f : f;
+      // 2^(11 - e2) in two factors: neither leaves fp32's range (e2 is at least -133)
+      const int up = 11 - e2;
+      const float up1 = __uint_as_float((uint32_t)(up / 2 + 127) << 23) * sign;
+      const float up2 = __uint_as_float((uint32_t)(up - up / 2 + 127) << 23);
       rf[0] = __shfl_sync(0xffffffffu, f, 8 * j);
       rf[1] = __shfl_sync(0xffffffffu, f, 8 * j + 4);
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[w][e] = ldexpf(x[w][e], 11 - e2) * sign;
+        for (int e = 0; e < 8; ++e) x[w][e] = x[w][e] * up1 * up2;
         // a word's codes come in the pairs (i, i + 4)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -448,10 +474,10 @@ kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
           float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int k = i * NW / NG; k < (i + 1) * NW / NG; ++k) {
-            mma16816(c, code_lo(w[0][k], z0), code_lo(w[1][k], z1), code_hi(w[0][k], z0), code_hi(w[1][k], z1),
+            mma16816(c, code_lo(w[0][k], masks, z0), code_lo(w[1][k], masks, z1), code_hi(w[0][k], masks, z0), code_hi(w[1][k], masks, z1),
                      qb[2 * k][0], qb[2 * k][1]);
             const uint32_t x = w[0][k] >> 8, y = w[1][k] >> 8;
-            mma16816(c, code_lo(x, z0), code_lo(y, z1), code_hi(x, z0), code_hi(y, z1), qb[2 * k + 1][0],
+            mma16816(c, code_lo(x, masks, z0), code_lo(y, masks, z1), code_hi(x, masks, z0), code_hi(y, masks, z1), qb[2 * k + 1][0],
                      qb[2 * k + 1][1]);
           }
           const float s0 = __low2float(p0), s1 = __low2float(p1);
@@ -558,8 +584,8 @@ kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
             const uint32_t p0 = pb[grp][h][0], p1 = pb[grp][h][1];
 #pragma unroll
             for (int i = 0; i < 4; i += 2) {
-              mma16816(acc[4 * f + i], code_lo(x0, za), code_lo(x1, za), code_lo(y0, zb), code_lo(y1, zb), p0, p1);
-              mma16816(acc[4 * f + i + 1], code_hi(x0, za), code_hi(x1, za), code_hi(y0, zb), code_hi(y1, zb), p0, p1);
+              mma16816(acc[4 * f + i], code_lo(x0, masks, za), code_lo(x1, masks, za), code_lo(y0, masks, zb), code_lo(y1, masks, zb), p0, p1);
+              mma16816(acc[4 * f + i + 1], code_hi(x0, masks, za), code_hi(x1, masks, za), code_hi(y0, masks, zb), code_hi(y1, masks, zb), p0, p1);
               x0 >>= 8; x1 >>= 8; y0 >>= 8; y1 >>= 8;
             }
           }
@@ -575,7 +601,7 @@ kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
             uint32_t y0 = __byte_perm(wc, wd, 0x5410) >> sh, y1 = __byte_perm(wc, wd, 0x7632) >> sh;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              mma16816(acc[2 * q + i], code_lo(x0, za), code_lo(x1, za), code_lo(y0, zb), code_lo(y1, zb),
+              mma16816(acc[2 * q + i], code_lo(x0, masks, za), code_lo(x1, masks, za), code_lo(y0, masks, zb), code_lo(y1, masks, zb),
                        pb[q][h][0], pb[q][h][1]);
               x0 >>= 8; x1 >>= 8; y0 >>= 8; y1 >>= 8;
             }
