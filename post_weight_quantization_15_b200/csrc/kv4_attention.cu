@@ -620,6 +620,9 @@ kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
 #pragma unroll
+    for (int r = 0; r < 2; ++r)
+      if (l[r] != l[r]) m[r] = 0.f;       // a NaN score: a part without a maximum would not count
+#pragma unroll
     for (int a = 0; a < MT; ++a) {
       const int i = a * NG / MT;
       const float mul = ve[i] < -116 ? 0.f : __uint_as_float((uint32_t)(ve[i] - 10 + 127) << 23);   // unset: acc is 0
@@ -705,11 +708,14 @@ kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
 }
 
 // Joins the parts of one query row whose tiles fell to several blocks; writes the rows of
-// sequences without tokens.  One block per row: warp w takes the parts w, w + 8, ...
+// sequences without tokens.  One block per row: every part's maximum and sum at once, then a
+// warp w the values of parts w, w + 8, ..., several in flight.
 template <int D>
 __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
   constexpr int V = D / 32;               // values per lane
+  constexpr int MOST = RUNS / WARPS + 2;  // parts of a row
   __shared__ float o[8][D];
+  __shared__ float weight[MOST];
   __shared__ float ml[8][2];
   __shared__ long long sums[8][2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -753,34 +759,57 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ K
   if (c0 == c1) return;                   // finished by its warp
   // the parts: run c0's, those of the blocks after it (their first run's), and the last run's
   const int parts = 2 + (c1 - 1) / WARPS - c0 / WARPS;
-  float m = -INFINITY, l = 0.f, x[V];
+  auto slot_of = [&](int i) {
+    return (int64_t)(i == parts - 1 ? 2 * c1 : 2 * (i == 0 ? c0 : (c0 / WARPS + i) * WARPS) + 1) * A.rows + row;
+  };
+  float top = -INFINITY;
+  for (int i = (int)threadIdx.x; i < parts; i += 256) {
+    weight[i] = A.part_ml[slot_of(i) * 2];
+    top = fmaxf(top, weight[i]);
+  }
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+  if (lane == 0) ml[warp][0] = top;
+  __syncthreads();
+  for (int w = 0; w < 8; ++w) top = fmaxf(top, ml[w][0]);
+  float sum = 0.f;
+  for (int i = (int)threadIdx.x; i < parts; i += 256) {
+    const float f = weight[i] == -INFINITY ? 0.f : ex2(weight[i] - top);
+    weight[i] = f;
+    sum = fmaf(A.part_ml[slot_of(i) * 2 + 1], f, sum);
+  }
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+  if (lane == 0) ml[warp][1] = sum;
+  __syncthreads();
+  float x[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) x[e] = 0.f;
 #pragma unroll 4
   for (int i = warp; i < parts; i += 8) {
-    const int64_t slot = i == parts - 1 ? 2 * c1 : 2 * (i == 0 ? c0 : (c0 / WARPS + i) * WARPS) + 1;
-    const int64_t p = slot * A.rows + row;
-    const float pm = A.part_ml[p * 2], pl = A.part_ml[p * 2 + 1];
-    const float mn = fmaxf(m, pm), ref = mn == -INFINITY ? 0.f : mn;
-    const float f = ex2(m - ref), w = ex2(pm - ref);
-    m = mn;
-    l = l * f + pl * w;
+    const float* part = A.part_o + slot_of(i) * D + lane * V;
+    const float f = weight[i];
+    float y[V];
+    if constexpr (V == 4) {
+      const float4 v4 = *reinterpret_cast<const float4*>(part);
+      y[0] = v4.x; y[1] = v4.y; y[2] = v4.z; y[3] = v4.w;
+    } else {
+      const float2 v2 = *reinterpret_cast<const float2*>(part);
+      y[0] = v2.x; y[1] = v2.y;
+    }
 #pragma unroll
-    for (int e = 0; e < V; ++e) x[e] = x[e] * f + A.part_o[p * D + e * 32 + lane] * w;
+    for (int e = 0; e < V; ++e) x[e] = fmaf(y[e], f, x[e]);
   }
-  if (lane == 0) { ml[warp][0] = m; ml[warp][1] = l; }
 #pragma unroll
-  for (int e = 0; e < V; ++e) o[warp][e * 32 + lane] = x[e];
+  for (int e = 0; e < V; ++e) o[warp][lane * V + e] = x[e];
   __syncthreads();
   if ((int)threadIdx.x >= D / 8) return;
-  float top = -INFINITY, sum = 0.f, y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int w = 0; w < 8; ++w) top = fmaxf(top, ml[w][0]);
+  float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  sum = 0.f;
   for (int w = 0; w < 8; ++w) {
-    if (ml[w][0] == -INFINITY) continue;
-    const float f = ex2(ml[w][0] - top);
-    sum += ml[w][1] * f;
+    sum += ml[w][1];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] += o[w][threadIdx.x * 8 + e] * f;
+    for (int e = 0; e < 8; ++e) y[e] += o[w][threadIdx.x * 8 + e];
   }
   const float inv = top == -INFINITY ? 0.f : 1.f / sum;
 #pragma unroll

@@ -557,6 +557,32 @@ def test_kv4_attention_rows_behind_the_end_and_extremes():
         _close(o, ref, tol, mul)
 
 
+@pytest.mark.parametrize("n", [100, 5000, 40000])
+def test_kv4_attention_nan_stays_in_its_rows(n):
+    """A NaN in a query makes that head's result NaN, one in a group of values that group's features,
+    whatever blocks the tokens fall to; every other result stays as it was."""
+    rng = np.random.default_rng(n)
+    cache, table, k64, v64 = _kv_cache(rng, [n, 64], 2, 128, 64, 32, HF)
+    q = _rand(rng, (2, 8, 128), HF)
+    clean = G.kv4_attention(q, cache, table, _int([n, 64]))
+    ref, tol = _attn_tol(_np(q), k64, v64, [0, 1, 2], _cu([n, 64]), 128 ** -0.5, False, HF, 2.0 ** -11, dq=2.0 ** -25,
+                         small=2.0 ** -33)
+    q2 = q.clone()
+    q2[0, 3, 5] = float("nan")
+    got = G.kv4_attention(q2, cache, table, _int([n, 64]))
+    assert torch.isnan(got[0, 3]).all()
+    got[0, 3] = clean[0, 3]
+    # the heads of one k/v head move their kept maxima together: head 3's no longer moves the others'
+    _close(got, ref, tol, "other heads")
+    assert torch.equal(got[0, 4:], clean[0, 4:]) and torch.equal(got[1], clean[1])
+    pg, r = int(table[0, (n - 3) // 32]), (n - 3) % 32
+    cache.v_params[pg, 1, r, 1, 0] = float("nan")
+    got = G.kv4_attention(q, cache, table, _int([n, 64]))
+    assert torch.isnan(got[0, 4:, 64:]).all()
+    got[0, 4:, 64:] = clean[0, 4:, 64:]
+    assert torch.equal(got, clean)
+
+
 def test_kv4_attention_records_bad_lengths_and_pages():
     rng = np.random.default_rng(10)
     lens = [40, 20, 30]
