@@ -15,9 +15,17 @@
 //   warps 0-3, 4-7   one tile each, a thread per query: S from TMEM, the softmax in
 //                    registers, P back over S as 16-bit values, and at the end O / l;
 //   warp 8           TMA loads of Q (once) and a ring of K and V tiles;
-//   warp 9           one thread issues the products: S = Q K^T (both from shared memory),
-//                    O += P V (P from TMEM, V from shared memory with its features
-//                    contiguous).  While one tile is in its softmax, the other's products run.
+//   warp 9           issues the products: S = Q K^T (both from shared memory), O += P V (P
+//                    from TMEM, V from shared memory with its features contiguous; the first
+//                    64 keys' part as soon as their weights are there).  While one tile is in
+//                    its softmax, the other's products run.
+// Waits are polled by all lanes of a warp at once: polled by one lane, with the result passed
+// on, they cost 12% of the whole (16 x 2048 tokens x 32 heads: 795 us, then 730, 700 with the
+// products issued by one elected thread, 680 with the weights in two parts).  What bounds it:
+// the chain of one tile, about 2300 cycles of softmax (1024 of them exponentials) and 1500
+// for 16 products of 64 cycles and their latencies, of which the other tile hides half.
+// Tried and slower: a quarter of the exponentials as polynomials on the fma units (+2%), two
+// threads per query (+6%: the exchange of maxima).
 // Every wait is bounded (GPTQ_ERR_TIMEOUT).
 //
 // Few queries over many keys leave SMs idle: then a cluster of 2, 4 or 8 blocks shares a pair
@@ -50,6 +58,7 @@ constexpr int TQ = 128;                   // queries of a tile, keys of a tile
 constexpr int ATHREADS = 320;
 constexpr int SMS = 148;
 constexpr float LOG2E = 1.4426950408889634f;
+constexpr int MOST = 64;                  // keys whose weights are handed over first
 constexpr float KEEP = 8.f;               // log2 of the largest weight under a kept maximum
 
 template <int KD>
@@ -62,6 +71,7 @@ struct AttnSmem {
   uint64_t kv_full[kStages];
   uint64_t kv_empty[kStages];
   uint64_t s_full[2];
+  uint64_t p_most[2];                     // the weights of the first MOST keys are in TMEM
   uint64_t p_full[2];
   uint64_t o_full[2];
   uint64_t v_clean;
@@ -69,6 +79,7 @@ struct AttnSmem {
   uint32_t tmem_base;
   int abort;
   int skip;
+  int q_armed[2], kv_armed, committed;    // loads issued, products committed: what an abort waits for
   int valid;                              // this block's part of a shared pair of tiles is there
   int seq, tile;                          // this block's sequence and pair of tiles (-1: none)
 };
@@ -184,11 +195,16 @@ __device__ __forceinline__ bool drain_wait(uint64_t* bar, uint32_t parity) {
   return true;
 }
 
-// A whole warp waits for a barrier's phase (lane 0 polls).
+// A whole warp waits for a barrier's phase.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = tc::mbar_wait(bar, parity, abort_flag);
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort_flag));
+}
+
+// One thread of a whole warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 
 // The sequence and the pair of tiles of slot `slot` (sequences in order, a sequence's
@@ -400,9 +416,11 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
       S.tile = tile;
       S.skip = seq < 0 || has_error(st);
       S.abort = 0;
+      S.q_armed[0] = S.q_armed[1] = S.kv_armed = S.committed = 0;
       for (int i = 0; i < 2; ++i) {
         tc::mbar_init(&S.q_full[i], 1);
         tc::mbar_init(&S.s_full[i], 1);
+        tc::mbar_init(&S.p_most[i], 4);
         tc::mbar_init(&S.p_full[i], 4);
         tc::mbar_init(&S.o_full[i], 1);
       }
@@ -417,11 +435,6 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
   tc::tc_fence_after();
   const uint32_t taddr = S.tmem_base;
   volatile int* abort_flag = &S.abort;
-  int armed[NST];
-#pragma unroll
-  for (int i = 0; i < NST; ++i) armed[i] = 0;
-  bool q_armed[2] = {false, false};
-  bool mma_committed = false;
 
   if (!S.skip) {
     const int q0 = A.cu_q[S.seq], k0 = A.cu_k[S.seq];
@@ -446,7 +459,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
 #pragma unroll
             for (int c = 0; c < KD / 64; ++c)
               tma_load_3d(S.q[it] + c * (TQ * 128), &tq, &S.q_full[it], c * 64, h, q0 + tl[it].row0);
-            q_armed[it] = true;
+            S.q_armed[it] = 1;
           }
           const int s = it % NST;
           if (!tc::mbar_wait(&S.kv_empty[s], ((uint32_t)(it / NST) & 1u) ^ 1u, abort_flag)) break;
@@ -455,8 +468,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
 #pragma unroll
           for (int c = 0; c < KD / 64; ++c)
             tma_load_3d(S.kv[s] + c * (TQ * 128), map, &S.kv_full[s], c * 64, hk, k0 + first + (it >> 1) * TQ);
-#pragma unroll
-          for (int i = 0; i < NST; ++i) armed[i] += i == s;
+          S.kv_armed = it + 1;
         }
       }
       __syncwarp();
@@ -472,16 +484,22 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
         }
       }
     } else if (warp == 9) {
-      if (lane == 0) {
+      // The whole warp walks the loop, so that the products' descriptors stay in uniform
+      // registers, and one elected thread issues (under a branch on the lane every product cost
+      // about 90 cycles to issue, 64 to run).
+      {
+        const bool one = elect_one();
         // S of tile t from the key tile in stage s
         auto product_s = [&](int t, int s) {
-          const uint32_t a0 = tc::smem_u32(S.q[t]), b0 = tc::smem_u32(S.kv[s]);
+          const uint64_t a0 = tc::sdesc_k_sw128(tc::smem_u32(S.q[t])), b0 = tc::sdesc_k_sw128(tc::smem_u32(S.kv[s]));
+          if (one) {
 #pragma unroll
-          for (int k = 0; k < KD / 16; ++k) {
-            const uint32_t off = (k / 4) * (TQ * 128) + (k % 4) * 32;
-            tc::mma_f16(taddr + t * TQ, tc::sdesc_k_sw128(a0 + off), tc::sdesc_k_sw128(b0 + off), IDESC_S, k > 0);
+            for (int k = 0; k < KD / 16; ++k) {
+              const uint32_t off = ((k / 4) * (TQ * 128) + (k % 4) * 32) >> 4;   // in the descriptor's units
+              tc::mma_f16(taddr + t * TQ, a0 + off, b0 + off, IDESC_S, k > 0);
+            }
+            tc::mma_commit(&S.s_full[t]);
           }
-          tc::mma_commit(&S.s_full[t]);
         };
         bool ok = blocks > 0;
         if (ok) ok = tc::mbar_wait(&S.kv_full[0], 0, abort_flag);
@@ -492,7 +510,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
           tc::tc_fence_after();
           product_s(t, 0);
         }
-        if (ok) tc::mma_commit(&S.kv_empty[0]);
+        if (ok && one) tc::mma_commit(&S.kv_empty[0]);
         for (int j = 0; j < blocks && ok; ++j) {
           const int iv = 2 * j + 1, ik = 2 * j + 2;
           const int sv = iv % NST, sk = ik % NST;
@@ -501,25 +519,36 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
           if (ok && j + 1 < blocks) ok = tc::mbar_wait(&S.kv_full[sk], (uint32_t)(ik / NST) & 1u, abort_flag);
           for (int t = 0; t < 2 && ok; ++t) {
             if (j < tl[t].blocks) {
+              const uint64_t b0 = sdesc_mn_sw128(tc::smem_u32(S.kv[sv]), TQ * 128);
+              ok = tc::mbar_wait(&S.p_most[t], (uint32_t)j & 1u, abort_flag);
+              if (!ok) break;
+              tc::tc_fence_after();
+              if (one) {
+#pragma unroll
+                for (int k = 0; k < MOST / 16; ++k)
+                  mma_f16_ts(taddr + O_COL + t * KD, taddr + t * TQ + k * 8, b0 + (k * 2048 >> 4), IDESC_O, j > 0 || k > 0);
+              }
               ok = tc::mbar_wait(&S.p_full[t], (uint32_t)j & 1u, abort_flag);
               if (!ok) break;
               tc::tc_fence_after();
-              const uint32_t b0 = tc::smem_u32(S.kv[sv]);
+              if (one) {
 #pragma unroll
-              for (int k = 0; k < TQ / 16; ++k)
-                mma_f16_ts(taddr + O_COL + t * KD, taddr + t * TQ + k * 8, sdesc_mn_sw128(b0 + k * 2048, TQ * 128),
-                           IDESC_O, j > 0 || k > 0);
-              if (j + 1 == tl[t].blocks) tc::mma_commit(&S.o_full[t]);
+                for (int k = MOST / 16; k < TQ / 16; ++k)
+                  mma_f16_ts(taddr + O_COL + t * KD, taddr + t * TQ + k * 8, b0 + (k * 2048 >> 4), IDESC_O, true);
+                if (j + 1 == tl[t].blocks) tc::mma_commit(&S.o_full[t]);
+              }
             }
-            if (t == 1) tc::mma_commit(&S.kv_empty[sv]);
+            if (t == 1 && one) tc::mma_commit(&S.kv_empty[sv]);
             if (j + 1 < tl[t].blocks) product_s(t, sk);
-            if (t == 1 && j + 1 < blocks) tc::mma_commit(&S.kv_empty[sk]);
+            if (t == 1 && j + 1 < blocks && one) tc::mma_commit(&S.kv_empty[sk]);
           }
         }
         // every commit has arrived before the block's shared memory is given up
-        tc::mma_commit(&S.drain);
-        mma_committed = true;
-        if (!*abort_flag) drain_wait(&S.drain, 0);
+        if (one) {
+          tc::mma_commit(&S.drain);
+          S.committed = 1;
+          if (!*abort_flag) drain_wait(&S.drain, 0);
+        }
       }
     } else {
       const int t = warp >> 2;                            // warps 0-3: tile 0, 4-7: tile 1
@@ -550,12 +579,11 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
 #pragma unroll
           for (int i = 0; i < TQ; ++i) s[i] = i < see ? s[i] : -INFINITY;
         }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
+        float mx[4] = {m, m, m, m};
 #pragma unroll
-        for (int i = 4; i < TQ; i += 8) {
+        for (int i = 0; i < TQ; i += 8) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mx[e] = fmaxf(mx[e], i + 4 + e < TQ ? fmaxf(s[i + e], s[i + 4 + e]) : s[i + e]);
+          for (int e = 0; e < 4; ++e) asm("max.f32 %0, %0, %1, %2;" : "+f"(mx[e]) : "f"(s[i + 2 * e]), "f"(s[i + 2 * e + 1]));
         }
         const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
         if (j == 0) {
@@ -594,6 +622,12 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             p[e] = pack2(a, b, T());
           }
           tmem_st16(ts + i / 2, p);
+          if (i + 32 == MOST) {                           // their product may begin
+            tmem_st_wait();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&S.p_most[t]);
+          }
         }
         float a, b;
         unpack_f32x2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
@@ -671,13 +705,12 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
   __syncthreads();
   if (*abort_flag) {
     if (warp == 8 && lane == 0) {
-#pragma unroll
-      for (int i = 0; i < NST; ++i)
-        if (armed[i] > 0) drain_wait(&S.kv_full[i], (uint32_t)(armed[i] - 1) & 1u);
+      for (int it = max(0, S.kv_armed - NST); it < S.kv_armed; ++it)
+        drain_wait(&S.kv_full[it % NST], (uint32_t)(it / NST) & 1u);
       for (int i = 0; i < 2; ++i)
-        if (q_armed[i]) drain_wait(&S.q_full[i], 0);
+        if (S.q_armed[i]) drain_wait(&S.q_full[i], 0);
     }
-    if (warp == 9 && lane == 0 && mma_committed) drain_wait(&S.drain, 0);
+    if (warp == 9 && lane == 0 && S.committed) drain_wait(&S.drain, 0);
     if (threadIdx.x == 0) set_error(st, GPTQ_ERR_TIMEOUT, blockIdx.x, STAGE_ATTENTION);
     __syncthreads();
   }
