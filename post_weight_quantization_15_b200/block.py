@@ -132,14 +132,15 @@ def add_norm(X: torch.Tensor, weight: torch.Tensor, Y: Optional[torch.Tensor] = 
         raise ValueError("post_bias belongs to post_weight")
     if Y is not None:
         _rows(Y, tokens, d, "Y")
-    if weight.dtype not in _DTYPE_CODE:
+    pt = weight.dtype
+    if pt not in _DTYPE_CODE:
         raise ValueError("weight must be fp32/fp16/bf16")
-    for t, what in ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight"), (post_bias, "post_bias")):
-        if t is not None and (t.shape != (d,) or t.dtype != weight.dtype or not t.is_contiguous()):
-            raise ValueError(f"{what} must be a contiguous [{d}] tensor of weight's type")
+    for t in (weight, bias, post_weight, post_bias):
+        if t is not None and (t.dtype != pt or t.shape != (d,) or not t.is_contiguous()):
+            raise ValueError(f"weight, bias, post_weight and post_bias must be contiguous [{d}] tensors of one type")
     ld_gate = 0
     if gate is not None:
-        if gate.dtype != weight.dtype:
+        if gate.dtype != pt:
             raise ValueError("gate must have weight's type")
         if gate.dim() == 2:
             _rows(gate, tokens, d, "gate")
@@ -148,7 +149,7 @@ def add_norm(X: torch.Tensor, weight: torch.Tensor, Y: Optional[torch.Tensor] = 
             raise ValueError(f"gate must be a contiguous [{d}] or a [{tokens}, {d}] tensor")
     _status_ok(status)
     with _Launching(stream, X, weight, Y, post_weight, gate, bias, post_bias, x_out, out, status) as s:
-        given = [t for t in (out, x_out) if t is not None]
+        given = [t for t in (out, x_out) if t is not None] if out is not None or x_out is not None else ()
         if out is None:
             out = torch.empty_like(X, memory_format=torch.contiguous_format)
         if Y is not None and x_out is None:
@@ -162,11 +163,11 @@ def add_norm(X: torch.Tensor, weight: torch.Tensor, Y: Optional[torch.Tensor] = 
             _apart(out, X, Y, x_out, *par)
             same = x_out is not None and x_out.data_ptr() == X.data_ptr() and _ld(x_out, d) == _ld(X, d)
             _apart(x_out, None if same else X, Y, *par)
-        _check(lib().gptq_add_norm(_at(X), _DTYPE_CODE[X.dtype], _ld(X, d), _at(Y),
-                                   _DTYPE_CODE[Y.dtype if Y is not None else X.dtype], _ld(Y, d), _at(weight),
-                                   _at(bias), _at(post_weight), _at(post_bias), _at(gate), ld_gate,
-                                   _DTYPE_CODE[weight.dtype], tokens, d, float(alpha), float(eps), int(bool(center)),
-                                   _at(x_out), _ld(x_out, d), _at(out), _ld(out, d), _at(status), s),
+        code = _DTYPE_CODE[X.dtype]
+        _check(lib().gptq_add_norm(X.data_ptr(), code, _ld(X, d), _at(Y), code if Y is None else _DTYPE_CODE[Y.dtype],
+                                   _ld(Y, d), weight.data_ptr(), _at(bias), _at(post_weight), _at(post_bias),
+                                   _at(gate), ld_gate, _DTYPE_CODE[pt], tokens, d, float(alpha), float(eps), bool(center),
+                                   _at(x_out), _ld(x_out, d), out.data_ptr(), _ld(out, d), _at(status), s),
                "gptq_add_norm")
     return (X if Y is None else x_out), out
 
@@ -202,9 +203,9 @@ def rope_qkv(QKV: torch.Tensor, cos: Optional[torch.Tensor], sin: Optional[torch
         _ints(positions, (tokens,), "positions")
     _status_ok(status)
     with _Launching(stream, QKV, cos, sin, positions, bias, status) as s:
-        q = torch.empty((tokens, heads_q, head_dim), dtype=dtype, device=QKV.device)
-        k = torch.empty((tokens, heads_kv, head_dim), dtype=dtype, device=QKV.device)
-        v = torch.empty((tokens, heads_kv, head_dim), dtype=dtype, device=QKV.device)
+        q = QKV.new_empty((tokens, heads_q, head_dim), dtype=dtype)
+        k = QKV.new_empty((tokens, heads_kv, head_dim), dtype=dtype)
+        v = torch.empty_like(k)
         _check(lib().gptq_rope_qkv(_at(QKV), _DTYPE_CODE[QKV.dtype], _ld(QKV, cols), _at(bias), _at(cos),
                                    _at(sin), max_pos, rot, int(bool(interleaved)), _at(positions), tokens, heads_q,
                                    heads_kv, head_dim, _DTYPE_CODE[dtype], _at(q), _at(k), _at(v), _at(status),
@@ -357,7 +358,7 @@ def kv4_read(cache: KV4Cache, table: torch.Tensor, cu: torch.Tensor, tokens: int
     _status_ok(status)
     with _Launching(stream, cache.k_codes, cache.k_params, cache.v_codes, cache.v_params, table, cu, start,
                     status) as s:
-        k = torch.empty((int(tokens), desc.heads, desc.head_dim), dtype=dtype, device=cache.k_codes.device)
+        k = cache.k_codes.new_empty((int(tokens), desc.heads, desc.head_dim), dtype=dtype)
         v = torch.empty_like(k)
         _check(lib().gptq_kv4_read(ctypes.byref(desc), _at(table), table.shape[1], _at(cu), _at(start), count,
                                    int(tokens), _DTYPE_CODE[dtype], _at(k), _at(v), _at(status), s),
