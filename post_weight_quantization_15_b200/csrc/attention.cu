@@ -11,29 +11,33 @@
 // below 256 and the accumulated o needs no rescaling, which then is rare.
 //
 // A block takes 256 queries of one head as two tiles of 128, and the keys and values in
-// tiles of 128, on the tcgen05 tensor cores with the accumulators in TMEM:
+// tiles of 128, on the tcgen05 tensor cores with the accumulators in TMEM; then the next 256,
+// one block per SM going through all of them (in strides: neighbours share keys in L2):
 //   warps 0-3, 4-7   one tile each, a thread per query: S from TMEM, the softmax in
 //                    registers, P back over S as 16-bit values, and at the end O / l;
-//   warp 8           TMA loads of Q (once) and a ring of K and V tiles;
+//   warp 8           looks the pairs of tiles up and hands them out; TMA loads of Q and a ring
+//                    of K and V tiles, on into the next pair;
 //   warp 9           issues the products: S = Q K^T (both from shared memory), O += P V (P
 //                    from TMEM, V from shared memory with its features contiguous; the first
 //                    64 keys' part as soon as their weights are there).  While one tile is in
-//                    its softmax, the other's products run.
-// Waits are polled by all lanes of a warp at once: polled by one lane, with the result passed
-// on, they cost 12% of the whole (16 x 2048 tokens x 32 heads: 795 us, then 730, 700 with the
-// products issued by one elected thread, 680 with the weights in two parts).  What bounds it:
-// the chain of one tile, about 2300 cycles of softmax (1024 of them exponentials) and 1500
-// for 16 products of 64 cycles and their latencies, of which the other tile hides half.
-// Tried and slower: a quarter of the exponentials as polynomials on the fma units (+2%), two
-// threads per query (+6%: the exchange of maxima).
+//                    its softmax, the other's products run; while a pair is finished, the next
+//                    pair's first products.
 // Every wait is bounded (GPTQ_ERR_TIMEOUT).
+//
+// 16 x 2048 causal tokens x 32 heads of 128: 795 us with waits polled by one lane of a warp and
+// passed on, 730 polled by all lanes, 700 with the products issued by one elected thread, 680
+// with the weights handed over in two parts, 615 with blocks that stay (895 TFLOP/s); packed
+// sequences up to 6007, 64/8 heads: 1245, 1126, 1074, 1040, 1005 us (992 TFLOP/s).  What bounds
+// it: the chain of one tile, about 2300 cycles of softmax (1024 of them exponentials) and 1500 for
+// 16 products of 64 cycles and their latencies, of which the other tile hides half.  Tried and
+// not kept: a quarter of the exponentials as polynomials on the fma units (slower or even),
+// two threads per query (6% slower: the exchange of maxima), turns to and fro.
 //
 // Few queries over many keys leave SMs idle: then a cluster of 2, 4 or 8 blocks shares a pair
 // of tiles, each block taking a run of the key tiles; their (m, l, o) stay in shared memory,
 // and every block joins its share of the rows from all of them.  37 queries after 2011 keys,
-// 16 heads of 64: 39 us on one block per head, 16 on four; one query after 8000 keys, 8 heads
-// of 128: 148 us on one, 26 on eight; 2048 causal queries, 4 heads of 128: 45 us on one, 23 on
-// four.
+// 16 heads of 64: 39 us on one block per head, 16 on four (14 with what came after); one
+// query after 8000 keys, 8 heads of 128: 148 us on one, 26 (23) on eight.
 //
 // Rows that no query may see: scores of keys past a row's limit are replaced before they are
 // used; values past the sequence's end are zeroed in shared memory.  Inside a sequence a
@@ -56,10 +60,15 @@ namespace {
 
 constexpr int TQ = 128;                   // queries of a tile, keys of a tile
 constexpr int ATHREADS = 320;
-constexpr int SMS = 148;
+constexpr int SMS = 148;                  // blocks, one to an SM, that go through the pairs of tiles
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr int MOST = 64;                  // keys whose weights are handed over first
 constexpr float KEEP = 8.f;               // log2 of the largest weight under a kept maximum
+
+// A pair of tiles of one head: its sequence's first rows and lengths (pair -1: no more).
+struct Work {
+  int pair, h, q0, k0, lq, lk;
+};
 
 template <int KD>
 struct AttnSmem {
@@ -74,14 +83,17 @@ struct AttnSmem {
   uint64_t p_most[2];                     // the weights of the first MOST keys are in TMEM
   uint64_t p_full[2];
   uint64_t o_full[2];
-  uint64_t v_clean;
+  uint64_t q_empty[2];
+  uint64_t work_full[2];
+  uint64_t work_empty[2];
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
   int skip;
   int q_armed[2], kv_armed, committed;    // loads issued, products committed: what an abort waits for
   int valid;                              // this block's part of a shared pair of tiles is there
-  int seq, tile;                          // this block's sequence and pair of tiles (-1: none)
+  Work work[2];                           // what the loader has handed out
+  Work mine;                              // a shared pair of tiles (SPLIT)
 };
 
 // One tile's place: its queries, what they see, and how many key tiles that takes.
@@ -154,6 +166,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
          "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t taddr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr) : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // D[tmem] (+)= A[tmem] . B[smem], kind::f16: A as 16-bit pairs per column, a row per lane.
@@ -207,19 +227,21 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// The sequence and the pair of tiles of slot `slot` (sequences in order, a sequence's
-// pairs from the last, which sees the most keys, to the first); whole warp.  Sequences with
-// bad bounds have no pairs and are recorded.
-__device__ __forceinline__ void find_work(const AttentionArgs& A, int slot, int32_t* st, int& seq, int& tile) {
+// Slot `slot` (the sequences in order, a sequence's pairs from the last, which sees the most
+// keys, to the first) of head h; whole warp.  Sequences with bad bounds have no pairs and are
+// recorded.
+__device__ __forceinline__ Work find_work(const AttentionArgs& A, int slot, int h, int32_t* st) {
   const int lane = threadIdx.x & 31;
-  seq = -1;
-  tile = 0;
+  Work w{-1, h, 0, 0, 0, 0};
   int base = 0;
   for (int b0 = 0; b0 < A.count; b0 += 32) {
     const int b = b0 + lane;
-    int pairs = 0;
+    int pairs = 0, q0 = 0, q1 = 0, k0 = 0, k1 = 0;
     if (b < A.count) {
-      const int q0 = A.cu_q[b], q1 = A.cu_q[b + 1], k0 = A.cu_k[b], k1 = A.cu_k[b + 1];
+      q0 = A.cu_q[b];
+      q1 = A.cu_q[b + 1];
+      k0 = A.cu_k[b];
+      k1 = A.cu_k[b + 1];
       if (q0 < 0 || q1 < q0 || q1 > A.total_q || k0 < 0 || k1 < k0 || k1 > A.total_k)
         set_error(st, GPTQ_ERR_INVALID_ARG, b, STAGE_ATTENTION);
       else
@@ -234,12 +256,16 @@ __device__ __forceinline__ void find_work(const AttentionArgs& A, int slot, int3
     const unsigned hit = __ballot_sync(0xffffffffu, base + incl > slot);
     if (hit) {
       const int src = __ffs(hit) - 1;
-      seq = b0 + src;
-      tile = __shfl_sync(0xffffffffu, base + incl - 1 - slot, src);
-      return;
+      w.pair = __shfl_sync(0xffffffffu, base + incl - 1 - slot, src);
+      w.q0 = __shfl_sync(0xffffffffu, q0, src);
+      w.k0 = __shfl_sync(0xffffffffu, k0, src);
+      w.lq = __shfl_sync(0xffffffffu, q1, src) - w.q0;
+      w.lk = __shfl_sync(0xffffffffu, k1, src) - w.k0;
+      return w;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
   }
+  return w;
 }
 
 __device__ __forceinline__ Tile make_tile(const AttentionArgs& A, int first, int lq, int lk) {
@@ -252,9 +278,36 @@ __device__ __forceinline__ Tile make_tile(const AttentionArgs& A, int first, int
   return t;
 }
 
+// The two tiles of a pair, as one block of `size` that share it takes them.
+struct Tiles {
+  Tile t[2];
+  int first;                              // this block's first key
+  int blocks;                             // key tiles
+  int tail;                               // the last tile of values reaches past the sequence's end: rows it has
+  __device__ __forceinline__ Tiles(const AttentionArgs& A, const Work& w, int size, int rank) {
+    t[0] = make_tile(A, w.pair * 2 * TQ, w.lq, w.lk);
+    t[1] = make_tile(A, w.pair * 2 * TQ + TQ, w.lq, w.lk);
+    first = 0;
+    if (size > 1) {
+      const int share = (max(t[0].blocks, t[1].blocks) + size - 1) / size;
+      first = rank * share * TQ;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) t[i].blocks = max(0, min(share, t[i].blocks - rank * share));
+    }
+    blocks = max(t[0].blocks, t[1].blocks);
+    tail = blocks > 0 && first + blocks * TQ > w.lk ? w.lk - first - (blocks - 1) * TQ : 0;
+  }
+};
+
+// Keys that query `row` of a pair sees (0 behind the sequence's end).
+__device__ __forceinline__ int seen_of(const AttentionArgs& A, const Work& w, int row) {
+  const int i = w.pair * 2 * TQ + row;
+  return i < w.lq ? max(0, min(w.lk, A.causal ? i + 1 + w.lk - w.lq : w.lk)) : 0;
+}
+
 // One query against the keys it sees, one after another, by a whole warp (see above).
 template <typename T>
-__device__ __noinline__ void seen_row(const AttentionArgs& A, int t, int h, int hk, int k0, int seen) {
+__device__ __forceinline__ void seen_row(const AttentionArgs& A, int t, int h, int hk, int k0, int seen) {
   const int lane = threadIdx.x & 31;
   const T* q = static_cast<const T*>(A.q) + t * A.q_ts + h * A.q_hs;
   float m = -INFINITY, l = 0.f;
@@ -321,7 +374,7 @@ __device__ __forceinline__ int part_at(int r, int piece) { return r * KD + ((pie
 // Joins a share of the rows of a pair of tiles from the parts of the cluster's blocks: a warp
 // per row.
 template <int KD, typename T>
-__device__ __forceinline__ void join_parts(const AttentionArgs& A, AttnSmem<KD>& S, int h, int hk) {
+__device__ __forceinline__ void join_parts(const AttentionArgs& A, AttnSmem<KD>& S) {
   constexpr int V = KD / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t size = cluster_size(), rank = tc::cluster_rank();
@@ -330,11 +383,11 @@ __device__ __forceinline__ void join_parts(const AttentionArgs& A, AttnSmem<KD>&
     asm volatile("ld.shared::cluster.b32 %0, [%1];"
                  : "=r"(ok) : "r"(tc::map_to_cta(tc::smem_u32(&S.valid), lane)) : "memory");
   if (!__all_sync(0xffffffffu, ok)) return;
-  const int q0 = A.cu_q[S.seq], k0 = A.cu_k[S.seq];
-  const int lq = A.cu_q[S.seq + 1] - q0, lk = A.cu_k[S.seq + 1] - k0;
-  const int rows = min(2 * TQ, lq - S.tile * 2 * TQ);
+  const int q0 = S.mine.q0, k0 = S.mine.k0, lq = S.mine.lq, lk = S.mine.lk, h = S.mine.h;
+  const int hk = h / (A.heads_q / A.heads_kv);
+  const int rows = min(2 * TQ, lq - S.mine.pair * 2 * TQ);
   for (int r = (int)rank + warp * (int)size; r < rows; r += (int)size * (ATHREADS / 32)) {
-    const int i = S.tile * 2 * TQ + r;                    // the query in its sequence
+    const int i = S.mine.pair * 2 * TQ + r;               // the query in its sequence
     const int limit = max(0, min(lk, A.causal ? i + 1 + lk - lq : lk));
     const uint32_t ml_at = tc::smem_u32(S.q[0]) + r * 8;
     // feature piece: V consecutive values per lane
@@ -393,7 +446,7 @@ __device__ __forceinline__ void join_parts(const AttentionArgs& A, AttnSmem<KD>&
 template <int KD, typename T, bool SPLIT>
 __global__ void __launch_bounds__(ATHREADS, 1)
 attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                 const __grid_constant__ CUtensorMap tv, const __grid_constant__ AttentionArgs A, int32_t* st) {
+                 const __grid_constant__ CUtensorMap tv, const __grid_constant__ AttentionArgs A, int pairs, int32_t* st) {
   using Smem = AttnSmem<KD>;
   constexpr int NST = Smem::kStages, TILE = Smem::kTile;
   constexpr uint32_t FMT = std::is_same<T, __half>::value ? 0 : 1;
@@ -404,123 +457,150 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
   Smem& S = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int size = SPLIT ? (int)cluster_size() : 1, rank = SPLIT ? (int)tc::cluster_rank() : 0;
-  const int pair = (int)blockIdx.x / size;
-  const int h = pair % A.heads_q, hk = h / (A.heads_q / A.heads_kv);
+  const int step = (int)gridDim.x / size;                 // pairs of tiles taken at once
+  int at = (int)blockIdx.x / size;                        // the loader's pair (of every head), then at + step, ...
+  Work w{-1, 0, 0, 0, 0, 0};
 
   if (warp == 9) tc::tmem_alloc<512>(&S.tmem_base);
-  if (warp == 0) {
-    int seq, tile;
-    find_work(A, pair / A.heads_q, h == 0 && rank == 0 ? st : nullptr, seq, tile);
-    if (lane == 0) {
-      S.seq = seq;
-      S.tile = tile;
-      S.skip = seq < 0 || has_error(st);
-      S.abort = 0;
-      S.q_armed[0] = S.q_armed[1] = S.kv_armed = S.committed = 0;
-      for (int i = 0; i < 2; ++i) {
-        tc::mbar_init(&S.q_full[i], 1);
-        tc::mbar_init(&S.s_full[i], 1);
-        tc::mbar_init(&S.p_most[i], 4);
-        tc::mbar_init(&S.p_full[i], 4);
-        tc::mbar_init(&S.o_full[i], 1);
-      }
-      for (int i = 0; i < NST; ++i) { tc::mbar_init(&S.kv_full[i], 1); tc::mbar_init(&S.kv_empty[i], 1); }
-      tc::mbar_init(&S.v_clean, 32);
-      tc::mbar_init(&S.drain, 1);
-      tc::fence_barrier_init();
+  if (warp == 8) w = find_work(A, at / A.heads_q, at % A.heads_q, at % A.heads_q == 0 && rank == 0 ? st : nullptr);
+  if (warp == 0 && lane == 0) {
+    S.skip = has_error(st);
+    S.abort = 0;
+    S.q_armed[0] = S.q_armed[1] = S.kv_armed = S.committed = 0;
+    S.mine.pair = -1;
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&S.q_full[i], 1);
+      tc::mbar_init(&S.q_empty[i], 1);
+      tc::mbar_init(&S.s_full[i], 1);
+      tc::mbar_init(&S.p_most[i], 4);
+      tc::mbar_init(&S.p_full[i], 4);
+      tc::mbar_init(&S.o_full[i], 1);
+      tc::mbar_init(&S.work_full[i], 1);
+      tc::mbar_init(&S.work_empty[i], 9);
     }
+    for (int i = 0; i < NST; ++i) { tc::mbar_init(&S.kv_full[i], 1); tc::mbar_init(&S.kv_empty[i], 1); }
+    tc::mbar_init(&S.drain, 1);
+    tc::fence_barrier_init();
   }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t taddr = S.tmem_base;
   volatile int* abort_flag = &S.abort;
+  // the n-th pair that the loader hands out (whole warp; given back with done(n)); false after the
+  // last, or on an abort
+  auto handed = [&](int n) {
+    const volatile Work& v = S.work[n & 1];
+    return Work{v.pair, v.h, v.q0, v.k0, v.lq, v.lk};
+  };
+  auto take = [&](int n) {
+    if (!warp_wait(&S.work_full[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag)) return false;
+    w = handed(n);
+    return w.pair >= 0;
+  };
+  auto done = [&](int n) {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&S.work_empty[n & 1]);
+  };
 
   if (!S.skip) {
-    const int q0 = A.cu_q[S.seq], k0 = A.cu_k[S.seq];
-    const int lq = A.cu_q[S.seq + 1] - q0, lk = A.cu_k[S.seq + 1] - k0;
-    Tile tl[2] = {make_tile(A, S.tile * 2 * TQ, lq, lk), make_tile(A, S.tile * 2 * TQ + TQ, lq, lk)};
-    int first = 0;                                        // this block's first key
-    if constexpr (SPLIT) {
-      const int share = (max(tl[0].blocks, tl[1].blocks) + size - 1) / size;
-      first = rank * share * TQ;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) tl[t].blocks = max(0, min(share, tl[t].blocks - rank * share));
-    }
-    const int blocks = max(tl[0].blocks, tl[1].blocks);
-    // the last tile of values reaches past the sequence's end: its rows there are zeroed
-    const int tail = blocks > 0 && first + blocks * TQ > lk ? lk - first - (blocks - 1) * TQ : 0;
-
     if (warp == 8) {
-      if (lane == 0) {
-        for (int it = 0; it < 2 * blocks; ++it) {
-          if (it < 2 && tl[it].blocks > 0) {
-            tc::mbar_arrive_expect_tx(&S.q_full[it], TILE);
+      int it = 0, q_uses[2] = {0, 0};                     // loads into the ring, into Q
+      for (int n = 0;; ++n) {
+        if (!warp_wait(&S.work_empty[n & 1], ((uint32_t)(n >> 1) & 1u) ^ 1u, abort_flag)) break;
+        if (lane == 0) {
+          S.work[n & 1] = w;
+          if (SPLIT && w.pair >= 0) S.mine = w;
+          tc::mbar_arrive(&S.work_full[n & 1]);
+        }
+        if (w.pair < 0) break;
+        const Tiles tl(A, w, size, rank);
+        const int hk = w.h / (A.heads_q / A.heads_kv);
+        int ok = 1;
+        if (lane == 0) {
+          for (int i = 0; i < 2 * tl.blocks && ok; ++i, ++it) {
+            if (i < 2 && tl.t[i].blocks > 0) {
+              ok = tc::mbar_wait(&S.q_empty[i], ((uint32_t)q_uses[i] & 1u) ^ 1u, abort_flag);
+              if (!ok) break;
+              tc::mbar_arrive_expect_tx(&S.q_full[i], TILE);
+#pragma unroll
+              for (int c = 0; c < KD / 64; ++c)
+                tma_load_3d(S.q[i] + c * (TQ * 128), &tq, &S.q_full[i], c * 64, w.h, w.q0 + tl.t[i].row0);
+              S.q_armed[i] = ++q_uses[i];
+            }
+            const int s = it % NST;
+            ok = tc::mbar_wait(&S.kv_empty[s], ((uint32_t)(it / NST) & 1u) ^ 1u, abort_flag);
+            if (!ok) break;
+            tc::mbar_arrive_expect_tx(&S.kv_full[s], TILE);
+            const CUtensorMap* map = (i & 1) ? &tv : &tk;
 #pragma unroll
             for (int c = 0; c < KD / 64; ++c)
-              tma_load_3d(S.q[it] + c * (TQ * 128), &tq, &S.q_full[it], c * 64, h, q0 + tl[it].row0);
-            S.q_armed[it] = 1;
+              tma_load_3d(S.kv[s] + c * (TQ * 128), map, &S.kv_full[s], c * 64, hk, w.k0 + tl.first + (i >> 1) * TQ);
+            S.kv_armed = it + 1;
           }
-          const int s = it % NST;
-          if (!tc::mbar_wait(&S.kv_empty[s], ((uint32_t)(it / NST) & 1u) ^ 1u, abort_flag)) break;
-          tc::mbar_arrive_expect_tx(&S.kv_full[s], TILE);
-          const CUtensorMap* map = (it & 1) ? &tv : &tk;
-#pragma unroll
-          for (int c = 0; c < KD / 64; ++c)
-            tma_load_3d(S.kv[s] + c * (TQ * 128), map, &S.kv_full[s], c * 64, hk, k0 + first + (it >> 1) * TQ);
-          S.kv_armed = it + 1;
         }
-      }
-      __syncwarp();
-      if (tail > 0) {
-        const int it = 2 * blocks - 1, s = it % NST;
-        if (warp_wait(&S.kv_full[s], (uint32_t)(it / NST) & 1u, abort_flag)) {
-          for (int i = tail * 8 + lane; i < TQ * 8; i += 32)
-#pragma unroll
-            for (int c = 0; c < KD / 64; ++c)
-              *reinterpret_cast<uint4*>(S.kv[s] + c * (TQ * 128) + i * 16) = make_uint4(0, 0, 0, 0);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          tc::mbar_arrive(&S.v_clean);
-        }
+        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+        at += step;
+        w.pair = -1;
+        if (!SPLIT && at < pairs)
+          w = find_work(A, at / A.heads_q, at % A.heads_q, at % A.heads_q == 0 ? st : nullptr);
       }
     } else if (warp == 9) {
       // The whole warp walks the loop, so that the products' descriptors stay in uniform
       // registers, and one elected thread issues (under a branch on the lane every product cost
       // about 90 cycles to issue, 64 to run).
-      {
-        const bool one = elect_one();
-        // S of tile t from the key tile in stage s
-        auto product_s = [&](int t, int s) {
-          const uint64_t a0 = tc::sdesc_k_sw128(tc::smem_u32(S.q[t])), b0 = tc::sdesc_k_sw128(tc::smem_u32(S.kv[s]));
-          if (one) {
+      const bool one = elect_one();
+      // S of tile t from the key tile in stage s; `last`: Q is not needed any more
+      auto product_s = [&](int t, int s, bool last) {
+        const uint64_t a0 = tc::sdesc_k_sw128(tc::smem_u32(S.q[t])), b0 = tc::sdesc_k_sw128(tc::smem_u32(S.kv[s]));
+        if (one) {
 #pragma unroll
-            for (int k = 0; k < KD / 16; ++k) {
-              const uint32_t off = ((k / 4) * (TQ * 128) + (k % 4) * 32) >> 4;   // in the descriptor's units
-              tc::mma_f16(taddr + t * TQ, a0 + off, b0 + off, IDESC_S, k > 0);
-            }
-            tc::mma_commit(&S.s_full[t]);
+          for (int k = 0; k < KD / 16; ++k) {
+            const uint32_t off = ((k / 4) * (TQ * 128) + (k % 4) * 32) >> 4;   // in the descriptor's units
+            tc::mma_f16(taddr + t * TQ, a0 + off, b0 + off, IDESC_S, k > 0);
           }
-        };
-        bool ok = blocks > 0;
-        if (ok) ok = tc::mbar_wait(&S.kv_full[0], 0, abort_flag);
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (tl[t].blocks == 0) continue;
-          ok = tc::mbar_wait(&S.q_full[t], 0, abort_flag);
-          if (!ok) break;
-          tc::tc_fence_after();
-          product_s(t, 0);
+          tc::mma_commit(&S.s_full[t]);
+          if (last) tc::mma_commit(&S.q_empty[t]);
         }
-        if (ok && one) tc::mma_commit(&S.kv_empty[0]);
+      };
+      bool ok = true;
+      int it = 0;                                         // the pair's first load in the ring
+      uint32_t q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
+      for (int n = 0; ok && take(n); ++n) {
+        const Tiles tl(A, w, size, rank);
+        done(n);
+        const int blocks = tl.blocks;
+        if (blocks == 0) continue;
+        ok = tc::mbar_wait(&S.kv_full[it % NST], (uint32_t)(it / NST) & 1u, abort_flag);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || tl.t[t].blocks == 0) continue;
+          ok = tc::mbar_wait(&S.q_full[t], q_uses[t] & 1u, abort_flag);
+          if (!ok) break;
+          ++q_uses[t];
+          tc::tc_fence_after();
+          product_s(t, it % NST, tl.t[t].blocks == 1);
+        }
+        if (ok && one) tc::mma_commit(&S.kv_empty[it % NST]);
         for (int j = 0; j < blocks && ok; ++j) {
-          const int iv = 2 * j + 1, ik = 2 * j + 2;
+          const int iv = it + 2 * j + 1, ik = it + 2 * j + 2;
           const int sv = iv % NST, sk = ik % NST;
           ok = tc::mbar_wait(&S.kv_full[sv], (uint32_t)(iv / NST) & 1u, abort_flag);
-          if (ok && tail > 0 && j == blocks - 1) ok = tc::mbar_wait(&S.v_clean, 0, abort_flag);
+          if (ok && tl.tail > 0 && j == blocks - 1) {     // rows behind the sequence's end, zeroed
+            for (int i = tl.tail * 8 + lane; i < TQ * 8; i += 32)
+#pragma unroll
+              for (int c = 0; c < KD / 64; ++c)
+                *reinterpret_cast<uint4*>(S.kv[sv] + c * (TQ * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+          }
           if (ok && j + 1 < blocks) ok = tc::mbar_wait(&S.kv_full[sk], (uint32_t)(ik / NST) & 1u, abort_flag);
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (j < tl[t].blocks) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!ok) break;
+            if (j < tl.t[t].blocks) {
               const uint64_t b0 = sdesc_mn_sw128(tc::smem_u32(S.kv[sv]), TQ * 128);
-              ok = tc::mbar_wait(&S.p_most[t], (uint32_t)j & 1u, abort_flag);
+              ok = tc::mbar_wait(&S.p_most[t], p_uses[t] & 1u, abort_flag);
               if (!ok) break;
               tc::tc_fence_after();
               if (one) {
@@ -528,175 +608,180 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 for (int k = 0; k < MOST / 16; ++k)
                   mma_f16_ts(taddr + O_COL + t * KD, taddr + t * TQ + k * 8, b0 + (k * 2048 >> 4), IDESC_O, j > 0 || k > 0);
               }
-              ok = tc::mbar_wait(&S.p_full[t], (uint32_t)j & 1u, abort_flag);
+              ok = tc::mbar_wait(&S.p_full[t], p_uses[t] & 1u, abort_flag);
               if (!ok) break;
+              ++p_uses[t];
               tc::tc_fence_after();
               if (one) {
 #pragma unroll
                 for (int k = MOST / 16; k < TQ / 16; ++k)
                   mma_f16_ts(taddr + O_COL + t * KD, taddr + t * TQ + k * 8, b0 + (k * 2048 >> 4), IDESC_O, true);
-                if (j + 1 == tl[t].blocks) tc::mma_commit(&S.o_full[t]);
+                if (j + 1 == tl.t[t].blocks) tc::mma_commit(&S.o_full[t]);
               }
             }
             if (t == 1 && one) tc::mma_commit(&S.kv_empty[sv]);
-            if (j + 1 < tl[t].blocks) product_s(t, sk);
+            if (j + 1 < tl.t[t].blocks) product_s(t, sk, j + 2 == tl.t[t].blocks);
             if (t == 1 && j + 1 < blocks && one) tc::mma_commit(&S.kv_empty[sk]);
           }
         }
-        // every commit has arrived before the block's shared memory is given up
-        if (one) {
-          tc::mma_commit(&S.drain);
-          S.committed = 1;
-          if (!*abort_flag) drain_wait(&S.drain, 0);
-        }
+        it += 2 * blocks;
+      }
+      // every commit has arrived before the block's shared memory is given up
+      __syncwarp();
+      if (one) {
+        tc::mma_commit(&S.drain);
+        S.committed = 1;
+        if (!*abort_flag) drain_wait(&S.drain, 0);
       }
     } else {
       const int t = warp >> 2;                            // warps 0-3: tile 0, 4-7: tile 1
-      const Tile& me = tl[t];
       const int r = (warp & 3) * 32 + lane;               // this thread's query in the tile
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t ts = taddr + lanes + t * TQ, to = taddr + lanes + O_COL + t * KD;
-      const int limit = r < me.rows ? max(0, min(lk, A.causal ? me.row0 + r + me.shift : lk)) : 0;
-      const float c0 = A.scale * LOG2E;
-      const float c = c0 > 0.f ? c0 : 1.f;
-      float m = -INFINITY, l = 0.f;
+      uint32_t s_uses = 0, o_uses = 0;
       bool ok = true;
-      for (int j = 0; j < me.blocks; ++j) {
-        ok = warp_wait(&S.s_full[t], (uint32_t)j & 1u, abort_flag);
-        if (!ok) break;
-        tc::tc_fence_after();
-        float s[TQ];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(ts + i * 32, s + i * 32);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_wait(s + i * 32);
-        if (!(c0 > 0.f)) {                                // a scale of 0 or below: the product first
-#pragma unroll
-          for (int i = 0; i < TQ; ++i) s[i] *= c0;
+      for (int n = 0; ok && take(n); ++n) {
+        int blocks, see0;                                 // key tiles; keys that this thread's query sees, from `first`
+        {
+          const Tiles tl(A, w, size, rank);
+          blocks = tl.t[t].blocks;
+          see0 = seen_of(A, w, t * TQ + r) - tl.first;
         }
-        const int see = limit - first - j * TQ;
-        if (__any_sync(0xffffffffu, see < TQ)) {
-#pragma unroll
-          for (int i = 0; i < TQ; ++i) s[i] = i < see ? s[i] : -INFINITY;
-        }
-        float mx[4] = {m, m, m, m};
-#pragma unroll
-        for (int i = 0; i < TQ; i += 8) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) asm("max.f32 %0, %0, %1, %2;" : "+f"(mx[e]) : "f"(s[i + 2 * e]), "f"(s[i + 2 * e + 1]));
-        }
-        const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-        if (j == 0) {
-          m = mn;
-        } else {
-          const bool up = (mn - m) * c > KEEP;            // -inf to finite included
-          if (__any_sync(0xffffffffu, up)) {
-            // S's arrival also says that the products into O issued before it are done
-            const float f = up ? exp2_approx((m - mn) * c) : 1.f;
-            if (up) m = mn;
-            l *= f;
-#pragma unroll 1
-            for (int i = 0; i < KD; i += 32) {
-              float o[32];
-              tmem_ld32(to + i, o);
-              tmem_wait(o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= f;
-              tmem_st32(to + i, o);
-            }
-          }
-        }
-        const float ref = m == -INFINITY ? 0.f : m * c;
-        const uint64_t c2 = pack_f32x2(c, c), r2 = pack_f32x2(-ref, -ref);
-        uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < TQ; i += 32) {
-          uint32_t p[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float a, b;
-            unpack_f32x2(fma2(pack_f32x2(s[i + 2 * e], s[i + 2 * e + 1]), c2, r2), a, b);
-            a = exp2_approx(a);
-            b = exp2_approx(b);
-            sum[e & 3] = add2(sum[e & 3], pack_f32x2(a, b));
-            p[e] = pack2(a, b, T());
-          }
-          tmem_st16(ts + i / 2, p);
-          if (i + 32 == MOST) {                           // their product may begin
-            tmem_st_wait();
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&S.p_most[t]);
-          }
-        }
-        float a, b;
-        unpack_f32x2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
-        l += a + b;
-        tmem_st_wait();
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&S.p_full[t]);
-      }
-      if constexpr (SPLIT) {
-        // both tiles' products are done with the shared memory that the parts go to
-        for (int u = 0; u < 2; ++u)
-          if (ok && tl[u].blocks > 0) ok = warp_wait(&S.o_full[u], 0, abort_flag);
-        if (ok) {
+        const float c0 = A.scale * LOG2E;
+        const float c = c0 > 0.f ? c0 : 1.f;
+        float m = -INFINITY, l = 0.f;
+        for (int j = 0; j < blocks; ++j) {
+          ok = warp_wait(&S.s_full[t], s_uses & 1u, abort_flag);
+          if (!ok) break;
+          ++s_uses;
           tc::tc_fence_after();
-          const int row = t * TQ + r;
-          reinterpret_cast<float2*>(S.q[0])[row] = make_float2(m * c, l);
-          float* part = reinterpret_cast<float*>(S.kv[0]);
-          if (me.blocks > 0) {
-#pragma unroll 1
-            for (int i = 0; i < KD; i += 32) {
-              float o[32];
-              tmem_ld32(to + i, o);
-              tmem_wait(o);
+          float s[TQ];
 #pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<float4*>(part + part_at<KD>(row, (i + e) / 4)) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            }
+          for (int i = 0; i < 4; ++i) tmem_ld32(ts + i * 32, s + i * 32);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_wait(s + i * 32);
+          if (!(c0 > 0.f)) {                                // a scale of 0 or below: the product first
+#pragma unroll
+            for (int i = 0; i < TQ; ++i) s[i] *= c0;
           }
-        }
-      } else if (ok && me.rows > 0) {
-        if (me.blocks > 0) ok = warp_wait(&S.o_full[t], 0, abort_flag);
-        if (ok) {
-          tc::tc_fence_after();
-          const bool mine = r < me.rows;
-          T* dst = static_cast<T*>(A.o) + (int64_t)(q0 + me.row0 + r) * A.o_ts + h * A.o_hs;
-          const float inv = 1.f / l;
-          bool nan = false;
+          const int see = see0 - j * TQ;
+          if (__any_sync(0xffffffffu, see < TQ)) {
+#pragma unroll
+            for (int i = 0; i < TQ; ++i) s[i] = i < see ? s[i] : -INFINITY;
+          }
+          float mx[4] = {m, m, m, m};
+#pragma unroll
+          for (int i = 0; i < TQ; i += 8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) asm("max.f32 %0, %0, %1, %2;" : "+f"(mx[e]) : "f"(s[i + 2 * e]), "f"(s[i + 2 * e + 1]));
+          }
+          const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          if (j == 0) {
+            m = mn;
+          } else {
+            const bool up = (mn - m) * c > KEEP;            // -inf to finite included
+            if (__any_sync(0xffffffffu, up)) {
+              // S's arrival also says that the products into O issued before it are done
+              const float f = up ? exp2_approx((m - mn) * c) : 1.f;
+              if (up) m = mn;
+              l *= f;
 #pragma unroll 1
-          for (int i = 0; i < KD; i += 32) {
-            float o[32];
-            if (me.blocks > 0) {
-              tmem_ld32(to + i, o);
-              tmem_wait(o);
-            }
-            if (limit == 0) {
+              for (int i = 0; i < KD; i += 32) {
+                float o[32];
+                tmem_ld32(to + i, o);
+                tmem_wait(o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = 0.f;
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                o[e] *= inv;
-                nan |= o[e] != o[e];
+                for (int e = 0; e < 32; ++e) o[e] *= f;
+                tmem_st32(to + i, o);
               }
             }
-            if (mine) {
+          }
+          const float ref = m == -INFINITY ? 0.f : m * c;
+          const uint64_t c2 = pack_f32x2(c, c), r2 = pack_f32x2(-ref, -ref);
+          uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-              for (int e = 0; e < 32; e += 8)
-                if (i + e < A.head_dim) store8(dst + i + e, o + e);
+          for (int i = 0; i < TQ; i += 32) {
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float a, b;
+              unpack_f32x2(fma2(pack_f32x2(s[i + 2 * e], s[i + 2 * e + 1]), c2, r2), a, b);
+              a = exp2_approx(a);
+              b = exp2_approx(b);
+              sum[e & 3] = add2(sum[e & 3], pack_f32x2(a, b));
+              p[e] = pack2(a, b, T());
+            }
+            tmem_st16(ts + i / 2, p);
+            if (i + 32 == MOST) {                           // their product may begin
+              tmem_st_wait();
+              tc::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive(&S.p_most[t]);
             }
           }
-          unsigned again = __ballot_sync(0xffffffffu, nan && mine);
-          __syncwarp();                                   // a row's first values before its second
-          while (again != 0) {
-            const int src = __ffs(again) - 1;
-            again &= again - 1;
-            seen_row<T>(A, q0 + me.row0 + (warp & 3) * 32 + src, h, hk, k0, __shfl_sync(0xffffffffu, limit, src));
+          float a, b;
+          unpack_f32x2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
+          l += a + b;
+          tmem_st_wait();
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&S.p_full[t]);
+        }
+        if constexpr (SPLIT) {
+          // both tiles' products are done with the shared memory that the parts go to
+          const Tiles tl(A, w, size, rank);
+          for (int u = 0; u < 2; ++u)
+            if (ok && tl.t[u].blocks > 0) ok = warp_wait(&S.o_full[u], 0, abort_flag);
+          if (ok) {
+            tc::tc_fence_after();
+            const int row = t * TQ + r;
+            reinterpret_cast<float2*>(S.q[0])[row] = make_float2(m * c, l);
+            float* part = reinterpret_cast<float*>(S.kv[0]);
+            if (blocks > 0) {
+#pragma unroll 1
+              for (int i = 0; i < KD; i += 32) {
+                float o[32];
+                tmem_ld32(to + i, o);
+                tmem_wait(o);
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                  *reinterpret_cast<float4*>(part + part_at<KD>(row, (i + e) / 4)) =
+                      make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              }
+            }
+          }
+        } else if (ok) {
+          if (blocks > 0) ok = warp_wait(&S.o_full[t], o_uses++ & 1u, abort_flag);
+          if (ok) {
+            tc::tc_fence_after();
+            const Work v = handed(n);
+            const int i0 = v.pair * 2 * TQ + t * TQ + r, limit = seen_of(A, v, t * TQ + r);
+            T* dst = static_cast<T*>(A.o) + (int64_t)(v.q0 + i0) * A.o_ts + v.h * A.o_hs;
+            const float inv = limit > 0 ? 1.f / l : 0.f;
+            bool nan = false;
+#pragma unroll 1
+            for (int i = 0; i < KD; i += 16) {
+              float o[16];
+              tmem_ld16_wait(to + i, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                o[e] = limit > 0 ? o[e] * inv : 0.f;
+                nan |= o[e] != o[e];
+              }
+              if (i0 < v.lq) {
+                if (i < A.head_dim) store8(dst + i, o);
+                if (i + 8 < A.head_dim) store8(dst + i + 8, o + 8);
+              }
+            }
+            unsigned again = __ballot_sync(0xffffffffu, nan && i0 < v.lq);
+            while (again != 0) {
+              const int src = __ffs(again) - 1;
+              again &= again - 1;
+              seen_row<T>(A, v.q0 + i0 - lane + src, v.h, v.h / (A.heads_q / A.heads_kv), v.k0, __shfl_sync(0xffffffffu, limit, src));
+            }
           }
         }
+        done(n);
       }
     }
   }
@@ -708,7 +793,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
       for (int it = max(0, S.kv_armed - NST); it < S.kv_armed; ++it)
         drain_wait(&S.kv_full[it % NST], (uint32_t)(it / NST) & 1u);
       for (int i = 0; i < 2; ++i)
-        if (S.q_armed[i]) drain_wait(&S.q_full[i], 0);
+        if (S.q_armed[i] > 0) drain_wait(&S.q_full[i], (uint32_t)(S.q_armed[i] - 1) & 1u);
     }
     if (warp == 9 && lane == 0 && S.committed) drain_wait(&S.drain, 0);
     if (threadIdx.x == 0) set_error(st, GPTQ_ERR_TIMEOUT, blockIdx.x, STAGE_ATTENTION);
@@ -719,10 +804,10 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     tc::tmem_dealloc<512>(taddr);
   }
   if constexpr (SPLIT) {
-    if (threadIdx.x == 0) S.valid = !S.skip && !*abort_flag;
+    if (threadIdx.x == 0) S.valid = !S.skip && !*abort_flag && S.mine.pair >= 0;
     __syncwarp();
     tc::cluster_sync();                                   // every block's part is there, or said not to be
-    join_parts<KD, T>(A, S, h, hk);
+    join_parts<KD, T>(A, S);
     __syncwarp();
     tc::cluster_sync();                                   // and has been read
   }
@@ -748,7 +833,7 @@ int launch(const AttentionArgs& A, const CUtensorMap& tq, const CUtensorMap& tk,
   const int64_t pairs = (A.total_q / (2 * TQ) + (int64_t)A.count) * A.heads_q + 1;
   if (pairs * size > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(pairs * size));
+  cfg.gridDim = dim3((unsigned)(SPLIT ? pairs * size : (pairs < SMS ? pairs : SMS)));
   cfg.blockDim = dim3(ATHREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -758,7 +843,7 @@ int launch(const AttentionArgs& A, const CUtensorMap& tq, const CUtensorMap& tk,
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = SPLIT ? 1 : 0;
-  GPTQ_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, A, st));
+  GPTQ_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, A, (int)pairs, st));
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
 }

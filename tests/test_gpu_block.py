@@ -335,6 +335,18 @@ def test_attention_few_queries_masked_rows_take_no_part(dt, d):
     assert torch.isnan(got[20:40, :2]).all() and torch.isnan(got[25:40, 2:]).all()
 
 
+@pytest.mark.parametrize("hq,hk,d,dt,causal", [(8, 2, 128, BF, True), (6, 6, 64, HF, True), (9, 3, 80, BF, False)])
+def test_attention_many_pairs_per_block(hq, hk, d, dt, causal):
+    """Far more pairs of tiles than SMs, of every size, empty sequences among them: blocks go from pair to pair."""
+    rng = np.random.default_rng(hq)
+    lens = [int(n) for n in rng.integers(0, 700, 70)]
+    past = [int(n) for n in rng.integers(-100, 300, 70)]
+    lens[3] = lens[41] = 0
+    past = [max(p, -n) for p, n in zip(past, lens)]
+    past[10] = -lens[10]                                     # a sequence without keys
+    test_attention(lens, past, hq, hk, d, dt, causal)
+
+
 def test_attention_large_scores_and_scale():
     """Scores in the thousands (weights 0 and 1), a negative and a zero scale."""
     q, k, v, cq, ck = _attn_inputs([140], [0], 2, 1, 128, HF)
