@@ -21,7 +21,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from .gptq import _DTYPE_CODE, _KV4, _check, _require_cuda, lib, workspace
+from .gptq import _DTYPE_CODE, _KV4, OK, GptqError, _check, _require_cuda, lib, workspace
 
 _16BIT = (torch.float16, torch.bfloat16)
 
@@ -66,7 +66,7 @@ def _at(t: Optional[torch.Tensor]):
 
 
 def _status_ok(status: Optional[torch.Tensor]):
-    if status is not None and (status.dtype != torch.int32 or status.numel() != 4 or not status.is_contiguous()):
+    if status is not None and (status.numel() != 4 or status.dtype != torch.int32 or not status.is_contiguous()):
         raise ValueError("status must be a contiguous int32 [4] tensor")
 
 
@@ -95,6 +95,11 @@ def _rows(t: torch.Tensor, tokens: int, d: int, what: str):
         if t.is_contiguous() or ((d == 1 or t.stride(1) == 1) and (tokens == 1 or t.stride(0) >= d)):
             return
     raise ValueError(f"{what} must be an fp32/fp16/bf16 [{tokens}, {d}] tensor with contiguous rows")
+
+
+def _vector(t: torch.Tensor, dtype, d: int):
+    if t.dtype != dtype or t.dim() != 1 or t.numel() != d or not t.is_contiguous():
+        raise ValueError(f"weight, bias, post_weight and post_bias must be contiguous [{d}] tensors of one type")
 
 
 def _ld(t: Optional[torch.Tensor], d: int) -> int:
@@ -135,9 +140,13 @@ def add_norm(X: torch.Tensor, weight: torch.Tensor, Y: Optional[torch.Tensor] = 
     pt = weight.dtype
     if pt not in _DTYPE_CODE:
         raise ValueError("weight must be fp32/fp16/bf16")
-    for t in (weight, bias, post_weight, post_bias):
-        if t is not None and (t.dtype != pt or t.shape != (d,) or not t.is_contiguous()):
-            raise ValueError(f"weight, bias, post_weight and post_bias must be contiguous [{d}] tensors of one type")
+    _vector(weight, pt, d)
+    if bias is not None:
+        _vector(bias, pt, d)
+    if post_weight is not None:
+        _vector(post_weight, pt, d)
+        if post_bias is not None:
+            _vector(post_bias, pt, d)
     ld_gate = 0
     if gate is not None:
         if gate.dtype != pt:
@@ -164,11 +173,13 @@ def add_norm(X: torch.Tensor, weight: torch.Tensor, Y: Optional[torch.Tensor] = 
             same = x_out is not None and x_out.data_ptr() == X.data_ptr() and _ld(x_out, d) == _ld(X, d)
             _apart(x_out, None if same else X, Y, *par)
         code = _DTYPE_CODE[X.dtype]
-        _check(lib().gptq_add_norm(X.data_ptr(), code, _ld(X, d), _at(Y), code if Y is None else _DTYPE_CODE[Y.dtype],
-                                   _ld(Y, d), weight.data_ptr(), _at(bias), _at(post_weight), _at(post_bias),
-                                   _at(gate), ld_gate, _DTYPE_CODE[pt], tokens, d, float(alpha), float(eps), bool(center),
-                                   _at(x_out), _ld(x_out, d), out.data_ptr(), _ld(out, d), _at(status), s),
-               "gptq_add_norm")
+        rc = lib().gptq_add_norm(X.data_ptr(), code, d if tokens <= 1 else X.stride(0), _at(Y),
+                                 code if Y is None else _DTYPE_CODE[Y.dtype], _ld(Y, d), weight.data_ptr(), _at(bias),
+                                 _at(post_weight), _at(post_bias), _at(gate), ld_gate, _DTYPE_CODE[pt], tokens, d,
+                                 float(alpha), float(eps), bool(center), _at(x_out), _ld(x_out, d) if given else d,
+                                 out.data_ptr(), _ld(out, d) if given else d, _at(status), s)
+    if rc != OK:
+        raise GptqError(rc, "gptq_add_norm")
     return (X if Y is None else x_out), out
 
 
