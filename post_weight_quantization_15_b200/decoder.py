@@ -1,0 +1,194 @@
+"""Whole decoder blocks: calibration through both halves, prompts into a 4-bit cache, single tokens.
+
+pipeline.py chains the solver over the MLP half of a block; here the attention half comes before it,
+with the operators of block.py between the quantized layers.  Activations are token-major,
+[tokens, features] bf16; a block of width d with hq query and hk k/v heads of D features is
+
+    h  = N(x; norm_attn)                         add_norm (RMS)
+    q, k, v = rotary(h . [Wq; Wk; Wv]^T)         linear_bf16 or qmatvec, rope_qkv
+    a  = softmax(q k^T / sqrt(D)) v              attention; kv4_attention over the cache
+    x' = x + a . Wo^T,  h' = N(x'; norm_mlp)     add_norm, one pass
+    x'' = x' + (silu(h' Wgate^T) * (h' Wup^T)) . Wdown^T
+
+    quantize_decoder_blocks   each layer calibrated on what the layers before it, quantized, produce
+    prompt_blocks             a packed batch of prompts through quantized blocks, into their caches
+    decode_blocks             one token of each of up to 16 sequences, against the caches
+
+Products with the dequantized weights run on the tensor cores (prompts), with the stored codes in
+qmatvec (single tokens).
+"""
+from __future__ import annotations
+
+import dataclasses
+from typing import Dict, List, Optional, Sequence, Tuple
+
+import torch
+
+from . import block as B
+from . import gptq as G
+
+
+@dataclasses.dataclass
+class DecoderWeights:
+    """One block's weights: layers [out, in] fp16/bf16/fp32, norms [d] (bf16, fp16 or fp32)."""
+    wq: torch.Tensor
+    wk: torch.Tensor
+    wv: torch.Tensor
+    wo: torch.Tensor
+    w_gate: torch.Tensor
+    w_up: torch.Tensor
+    w_down: torch.Tensor
+    norm_attn: torch.Tensor
+    norm_mlp: torch.Tensor
+
+
+@dataclasses.dataclass
+class Rotary:
+    """Heads of a block and its rotary tables, cos and sin fp32 [positions, rot / 2]."""
+    heads_q: int
+    heads_kv: int
+    head_dim: int
+    cos: Optional[torch.Tensor]
+    sin: Optional[torch.Tensor]
+    interleaved: bool = False
+
+
+@dataclasses.dataclass
+class QuantizedBlock:
+    qkv: G.QuantizedLayer          # q, k and v stacked along the outputs
+    o: G.QuantizedLayer
+    gate_up: G.QuantizedLayer      # gate's rows first
+    down: G.QuantizedLayer
+    norm_attn: torch.Tensor
+    norm_mlp: torch.Tensor
+    eps: float
+    stages: Optional[Dict[str, torch.Tensor]] = None   # what each stage gave (record=True)
+
+
+def _quantize(ws: Sequence[torch.Tensor], X: torch.Tensor, bits, group_size, sym, desc_act, damp, st):
+    """The layers ws quantized together on the token-major calibration input X; their processing order."""
+    n = X.shape[1]
+    H = torch.zeros((n, n), dtype=torch.float32, device=X.device)
+    hd = torch.zeros(n, dtype=torch.float64, device=X.device) if desc_act else None
+    G.hessian_accumulate(H, G.transpose_bf16(X, st), hd, st)
+    prep = G.prepare(H, damp, desc_act, hd, st)
+    if len(ws) == 1:
+        return G.quantize_layer(ws[0], prep, bits, group_size, sym), prep.perm
+    return G.quantize_layers(ws, prep, bits, group_size, sym)[0], prep.perm
+
+
+def _forward(q: G.QuantizedLayer, X: torch.Tensor, st) -> torch.Tensor:
+    """fp32 [tokens, out] = X . What^T, the weights dequantized to bf16."""
+    return G.linear_bf16(X, G.dequantize(q, torch.bfloat16, st), st)
+
+
+def _mlp_hidden(gate_up: G.QuantizedLayer, h: torch.Tensor, st) -> torch.Tensor:
+    What = G.dequantize(gate_up, torch.bfloat16, st)
+    f = What.shape[0] // 2
+    return G.silu_mul(G.linear_bf16(h, What[:f], st), G.linear_bf16(h, What[f:], st), st)
+
+
+def _check_stream(X: torch.Tensor):
+    if X.dim() != 2 or X.dtype != torch.bfloat16 or not X.is_contiguous():
+        raise ValueError("X must be a contiguous bf16 [tokens, d] tensor")
+    if not X.is_cuda:
+        raise ValueError("X must be a CUDA tensor")
+
+
+def quantize_decoder_blocks(X0: torch.Tensor, cu: torch.Tensor, blocks: Sequence[DecoderWeights], rotary: Rotary,
+                            positions: Optional[torch.Tensor] = None, eps: float = 1e-6, bits: int = 4,
+                            group_size: int = 128, sym: bool = True, desc_act: bool = True,
+                            damp_percent: float = 0.01, record: bool = False,
+                            status: Optional[torch.Tensor] = None) -> Tuple[List[QuantizedBlock], torch.Tensor]:
+    """Quantize decoder blocks in sequence; returns (the blocks, the last block's output).
+
+    X0 bf16 [tokens, d] (tokens a multiple of 8), the packed calibration sequences; cu int32
+    [sequences + 1] their first rows and the end; positions int32 [tokens] for the rotary tables
+    (None: row t is at position t).  decode_blocks takes desc_act blocks too, more slowly (qmatvec
+    reads their groups column by column).
+    """
+    _check_stream(X0)
+    st = status if status is not None else G.new_status(X0.device)
+    how = (bits, group_size, sym, desc_act, damp_percent, st)
+    r = rotary
+    x, y = X0, None                # the stream, and what is still to be added to it
+    out: List[QuantizedBlock] = []
+    for w in blocks:
+        x, h = B.add_norm(x, w.norm_attn, Y=y, eps=eps, status=st)
+        x_in = x
+        qkv, perm_qkv = _quantize([w.wq, w.wk, w.wv], h, *how)
+        q, k, v = B.rope_qkv(_forward(qkv, h, st), r.cos, r.sin, r.heads_q, r.heads_kv, r.head_dim, positions,
+                             interleaved=r.interleaved, status=st)
+        a = B.attention(q, k, v, cu, status=st).flatten(1)
+        o, perm_o = _quantize([w.wo], a, *how)
+        x_mid, h2 = B.add_norm(x, w.norm_mlp, Y=_forward(o, a, st), eps=eps, status=st)
+        gate_up, perm_gate_up = _quantize([w.w_gate, w.w_up], h2, *how)
+        m = _mlp_hidden(gate_up, h2, st)
+        down, perm_down = _quantize([w.w_down], m, *how)
+        x, y = x_mid, _forward(down, m, st)
+        out.append(QuantizedBlock(qkv, o, gate_up, down, w.norm_attn, w.norm_mlp, eps, dict(
+            x_in=x_in, h=h, q=q, k=k, v=v, a=a, x_mid=x_mid, h_mlp=h2, m=m, y=y, perm_qkv=perm_qkv, perm_o=perm_o,
+            perm_gate_up=perm_gate_up, perm_down=perm_down) if record else None))
+    X = x if y is None else G.residual_add(x, y, st)
+    G.raise_on_status(st, "quantize_decoder_blocks")
+    return out, X
+
+
+def prompt_blocks(X: torch.Tensor, cu: torch.Tensor, blocks: Sequence[QuantizedBlock], rotary: Rotary,
+                  positions: Optional[torch.Tensor] = None, caches: Optional[Sequence[B.KV4Cache]] = None,
+                  table: Optional[torch.Tensor] = None, start: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A packed batch of prompts, bf16 [tokens, d], through the blocks; returns the stream after them.
+
+    caches (one per block): the prompts' keys and values are appended at positions start[b] ...
+    (int32 [sequences]; None: 0) of sequence b, in the pages that table names.
+    """
+    _check_stream(X)
+    if caches is not None and (table is None or len(caches) != len(blocks)):
+        raise ValueError("caches need a table, and one cache per block")
+    r, y = rotary, None
+    if caches is not None and start is None:
+        start = torch.zeros(cu.numel() - 1, dtype=torch.int32, device=X.device)
+    for i, b in enumerate(blocks):
+        X, h = B.add_norm(X, b.norm_attn, Y=y, eps=b.eps, status=status)
+        q, k, v = B.rope_qkv(_forward(b.qkv, h, status), r.cos, r.sin, r.heads_q, r.heads_kv, r.head_dim, positions,
+                             interleaved=r.interleaved, status=status)
+        if caches is not None:
+            B.kv4_append(caches[i], k, v, table, cu, start, status=status)
+        a = B.attention(q, k, v, cu, status=status).flatten(1)
+        X, h = B.add_norm(X, b.norm_mlp, Y=_forward(b.o, a, status), eps=b.eps, status=status)
+        y = _forward(b.down, _mlp_hidden(b.gate_up, h, status), status)
+    return X if y is None else G.residual_add(X, y, status)
+
+
+def decode_blocks(X: torch.Tensor, lengths: torch.Tensor, blocks: Sequence[QuantizedBlock], rotary: Rotary,
+                  caches: Sequence[B.KV4Cache], table: torch.Tensor, ws: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token of each sequence, bf16 [sequences, d], through the blocks; returns the stream after them.
+
+    lengths int32 [sequences]: tokens of each sequence in the caches before this one, which is the
+    new token's position too; it is appended and attended to.  lengths itself is not advanced.
+    At most 16 sequences (qmatvec's rows).  ws: kv4_attention's workspace (a captured step needs its own).
+    """
+    _check_stream(X)
+    n = X.shape[0]
+    if n < 1 or n > 16:
+        raise ValueError("decode_blocks takes 1 to 16 sequences")
+    if len(caches) != len(blocks):
+        raise ValueError("decode_blocks needs one cache per block")
+    if lengths.dtype != torch.int32 or tuple(lengths.shape) != (n,):
+        raise ValueError("lengths must be int32 [sequences]")
+    r, y = rotary, None
+    cu = torch.arange(n + 1, dtype=torch.int32, device=X.device)
+    after = lengths + 1
+    for b, cache in zip(blocks, caches):
+        X, h = B.add_norm(X, b.norm_attn, Y=y, eps=b.eps, status=status)
+        q, k, v = B.rope_qkv(G.qmatvec(b.qkv, h, status), r.cos, r.sin, r.heads_q, r.heads_kv, r.head_dim, lengths,
+                             interleaved=r.interleaved, status=status)
+        B.kv4_append(cache, k, v, table, cu, lengths, status=status)
+        a = B.kv4_attention(q, cache, table, after, ws=ws, status=status).flatten(1)
+        X, h = B.add_norm(X, b.norm_mlp, Y=G.qmatvec(b.o, a, status), eps=b.eps, status=status)
+        gu = G.qmatvec(b.gate_up, h, status)
+        f = gu.shape[1] // 2
+        y = G.qmatvec(b.down, G.silu_mul(gu[:, :f].contiguous(), gu[:, f:].contiguous(), status), status)
+    return X if y is None else G.residual_add(X, y, status)

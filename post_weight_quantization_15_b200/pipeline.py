@@ -11,8 +11,8 @@ module chains the library's calls over the MLP half of Llama-shaped decoder bloc
         H = 2.h.h^T; prepare; down quantized
         X <- X + What_down . h                      the next block's input
 
-(The attention half is not a linear layer of the solver and is left out: its q, k, v
-and o layers need attention's own arithmetic between them.)  Every step is a library
+(The attention half's q, k, v and o layers need attention's own arithmetic between them:
+decoder.py chains both halves.)  Every step is a library
 kernel: the Hessian, preparation, sweep, dequantization, the bf16 tensor-core
 product, the transposes and the elementwise SiLU-gate and residual.  The steps are
 data-dependent one after the other (each layer's Hessian needs the previous layer's
