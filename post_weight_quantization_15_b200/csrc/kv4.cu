@@ -14,14 +14,14 @@
 // low bits, where the eight codes of a word are summed under their shifts (the constant's
 // and the zero point's shares taken off once).
 //
-// Bound: HBM, with the issue slots close behind.  A thread quantizes sixteen features of a
-// group, eight in each of its halves (two 16-byte loads side by side across the group's
-// group / 16 threads, two words of codes), of keys and values; the group's range is found with
-// shuffles on packed 16-bit values.  A block takes a few consecutive tokens, their places
-// looked up once.  (15,625 tokens of 32 heads x 128 in bf16, written and read back: 369 us with
-// one token per block, IEEE divisions and integer conversions; 203 with eight features per
-// thread, 134 of it the writing; now 148, 87 of it the writing, whose 65 million warp
-// instructions take 74% of the issue slots.)
+// Bound: HBM, with the issue slots close behind.  A thread quantizes 32 features of a group (16
+// where the group has no more), eight at a time and side by side with the group's other
+// threads, of keys and values; the group's range is found with shuffles on packed 16-bit
+// values.  What a group costs (its range, scale, zero point, addresses) is as much as sixteen
+// features do, hence so many per thread.  A block takes a few consecutive tokens, their places
+// looked up once.  (15,625 tokens of 32 heads x 128 in bf16, groups of 128, written and read back:
+// 369 us with one token per block, IEEE divisions and integer conversions; 203 with eight
+// features per thread, 148 with sixteen, 135 with 32; 99 at the copy bandwidth.)
 #include <type_traits>
 
 #include "common.cuh"
@@ -98,16 +98,23 @@ __device__ __forceinline__ float reciprocal(float x) {     // to 2^-23
   return r;
 }
 
-// Sixteen values of a group that `lanes` threads share -> their two words, and the group's scale
-// and zero point; `bad` if the group holds a NaN or an infinity.  Whole warp.
-template <typename T>
-__device__ __forceinline__ void quantize16(const uint4 (&raw)[2], int lanes, uint32_t (&word)[2], __half2& par,
-                                           bool& bad) {
-  const uint32_t w[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+// N times eight values of a group that `lanes` threads share -> their N words, and the group's
+// scale and zero point; `bad` if the group holds a NaN or an infinity.  Whole warp.
+template <typename T, int N>
+__device__ __forceinline__ void quantize(const uint4 (&raw)[N], int lanes, uint32_t (&word)[N], __half2& par,
+                                         bool& bad) {
+  uint32_t w[4 * N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    w[4 * i] = raw[i].x;
+    w[4 * i + 1] = raw[i].y;
+    w[4 * i + 2] = raw[i].z;
+    w[4 * i + 3] = raw[i].w;
+  }
   // (-smallest, largest) as one pair, 0 included
   uint32_t lo = w[0], hi = w[0];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
+  for (int i = 1; i < 4 * N; ++i) {
     lo = min2(lo, w[i], T());
     hi = max2(hi, w[i], T());
   }
@@ -133,7 +140,7 @@ __device__ __forceinline__ void quantize16(const uint4 (&raw)[2], int lanes, uin
   const float most = 15.f - z;
   const uint32_t offset = (zi - __float_as_uint(ROUND)) * 0x11111111u;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < N; ++h) {
     uint32_t sum = offset;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -152,7 +159,8 @@ __device__ __forceinline__ void quantize16(const uint4 (&raw)[2], int lanes, uin
   par = __halves2half2(s16, __float2half_rn(z));
 }
 
-template <typename T>
+// A thread takes N words of a group: w, w + lanes, ...
+template <typename T, int N>
 __global__ void __launch_bounds__(THREADS) kv4_append_kernel(const __grid_constant__ KV4Cache C,
                                                              const __grid_constant__ KVInput in, const int32_t* table,
                                                              int width, const int32_t* cu, const int32_t* start,
@@ -161,43 +169,45 @@ __global__ void __launch_bounds__(THREADS) kv4_append_kernel(const __grid_consta
   if (has_error(st)) return;
   const int t0 = (int)blockIdx.x * per_block, n = min(per_block, tokens - t0);
   find_rows(C, table, width, cu, start, count, t0, n, rows, st);
-  const Units U(C.heads * (C.head_dim / 16));
-  const int words = C.head_dim / 8, lanes = C.group / 16, groups = C.head_dim / C.group;
-  const int lw = __ffs(words / 2) - 1, ll = __ffs(lanes) - 1;
+  const Units U(C.heads * (C.head_dim / (8 * N)));
+  const int words = C.head_dim / 8, lanes = C.group / (8 * N), groups = C.head_dim / C.group;
+  const int lw = __ffs(words / N) - 1, ll = __ffs(lanes) - 1;
   // every thread goes through every step: the shuffles take whole warps
   for (int step = 0; step < U.per; step += THREADS) {
-    const int u = U.u0 + step, head = u >> lw, in_head = u & (words / 2 - 1);
-    const int group = in_head >> ll, lane = in_head & (lanes - 1), w = 2 * (group << ll) + lane;   // words w, w + lanes
+    const int u = U.u0 + step, head = u >> lw, in_head = u & (words / N - 1);
+    const int group = in_head >> ll, lane = in_head & (lanes - 1), w = N * (group << ll) + lane;
     for (int i0 = 0; i0 < n; i0 += U.subs) {
       const int i = i0 + U.sub;
       const int64_t row = u < U.per && U.sub < U.subs && i < n ? rows[i] : -1;
-      uint4 raw[2][2];
+      uint4 raw[2][N];
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        raw[kv][0] = raw[kv][1] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < N; ++c) raw[kv][c] = make_uint4(0, 0, 0, 0);
         if (row >= 0) {
           const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(in.p[kv]) +
                                                             (int64_t)(t0 + i) * in.token_stride[kv] +
                                                             head * in.head_stride[kv]) + w;
-          raw[kv][0] = __ldcs(src);
-          raw[kv][1] = __ldcs(src + lanes);
+#pragma unroll
+          for (int c = 0; c < N; ++c) raw[kv][c] = __ldcs(src + c * lanes);
         }
       }
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         __half2 par;
-        uint32_t word[2];
+        uint32_t word[N];
         bool bad;
-        quantize16<T>(raw[kv], lanes, word, par, bad);
+        quantize<T, N>(raw[kv], lanes, word, par, bad);
         if (row < 0) continue;
         if (bad) {                        // the whole group reads back as NaN
-          word[0] = word[1] = 0;
+#pragma unroll
+          for (int c = 0; c < N; ++c) word[c] = 0;
           par = __halves2half2(__ushort_as_half((unsigned short)0x7fffu), __ushort_as_half((unsigned short)0));
           if (lane == 0) set_error(st, GPTQ_ERR_NONFINITE, t0 + i, STAGE_KV4);
         }
         const int64_t at = row + (int64_t)head * C.page_size;
-        C.codes[kv][at * words + w] = (int32_t)word[0];
-        C.codes[kv][at * words + w + lanes] = (int32_t)word[1];
+#pragma unroll
+        for (int c = 0; c < N; ++c) C.codes[kv][at * words + w + c * lanes] = (int32_t)word[c];
         if (lane == 0) reinterpret_cast<__half2*>(C.params[kv])[at * groups + group] = par;
       }
     }
@@ -250,9 +260,9 @@ __global__ void __launch_bounds__(THREADS) kv4_read_kernel(const __grid_constant
   }
 }
 
-// Tokens of a block: as many as keep its threads busy, more while there are blocks to spare.
-int tokens_per_block(const KV4Cache& C, int tokens) {
-  const int per = C.heads * (C.head_dim / 16);
+// Tokens of a block whose threads take `features` each: as many as keep its threads busy, more while there are blocks to spare.
+int tokens_per_block(const KV4Cache& C, int tokens, int features) {
+  const int per = C.heads * (C.head_dim / features);
   int n = per < THREADS ? THREADS / per : 1;
   if (n > MOST) n = MOST;
   while (n * 2 <= MOST && n * (int64_t)per < 8 * THREADS && cdiv(tokens, n * 2) >= ENOUGH) n *= 2;
@@ -267,20 +277,20 @@ int launch_kv4_append(const KV4Cache& C, const void* k, int64_t k_ts, int64_t k_
                       int64_t v_hs, int dtype, int tokens, const int32_t* table, int width, const int32_t* cu,
                       const int32_t* start, int count, int32_t* st, cudaStream_t s) {
   const KVInput in{{k, v}, {k_ts, v_ts}, {k_hs, v_hs}};
-  const int n = tokens_per_block(C, tokens);
+  const int features = C.group >= 64 ? 32 : 16;
+  const int n = tokens_per_block(C, tokens, features);
   const unsigned grd = (unsigned)cdiv(tokens, n);
   TraceScope ts("kv4_append", "byte", tokens * (token_bytes(C) + 4.0 * C.heads * C.head_dim), s);
-  if (dtype == GPTQ_F16)
-    kv4_append_kernel<__half><<<grd, THREADS, 0, s>>>(C, in, table, width, cu, start, count, tokens, n, st);
-  else
-    kv4_append_kernel<__nv_bfloat16><<<grd, THREADS, 0, s>>>(C, in, table, width, cu, start, count, tokens, n, st);
+  auto go = [&](auto* kernel) { kernel<<<grd, THREADS, 0, s>>>(C, in, table, width, cu, start, count, tokens, n, st); };
+  if (dtype == GPTQ_F16) go(features == 32 ? kv4_append_kernel<__half, 4> : kv4_append_kernel<__half, 2>);
+  else go(features == 32 ? kv4_append_kernel<__nv_bfloat16, 4> : kv4_append_kernel<__nv_bfloat16, 2>);
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
 }
 
 int launch_kv4_read(const KV4Cache& C, const int32_t* table, int width, const int32_t* cu, const int32_t* start,
                     int count, int tokens, int dtype, void* k, void* v, int32_t* st, cudaStream_t s) {
-  const int n = tokens_per_block(C, tokens);
+  const int n = tokens_per_block(C, tokens, 16);
   const unsigned grd = (unsigned)cdiv(tokens, n);
   TraceScope ts("kv4_read", "byte", tokens * (token_bytes(C) + (dtype == GPTQ_F32 ? 8.0 : 4.0) * C.heads * C.head_dim), s);
   auto go = [&](auto* p) {
