@@ -442,10 +442,17 @@ kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
       auto& stage = S.ring[warp][s];
       const uint32_t kc = smem_addr(stage.codes[0]), vc = smem_addr(stage.codes[1]);
       const __half2* kp = stage.params[0];
-      const __half2* vp = stage.params[1];
+      __half2* vp = stage.params[1];
       // token i of the tile counts
       auto seen = [&](int i) { return i < have && ((ok >> (i >> 4)) & 1); };
 
+      if (edge) {                         // values that do not count: 0, whatever the page holds there
+        if (!seen(lane)) {
+#pragma unroll
+          for (int i = 0; i < NG; ++i) vp[lane * NG + i] = __float2half2_rn(0.f);
+        }
+        __syncwarp();
+      }
       // ---- scores: tokens 16 h + g (+ 8) against heads 2 j, 2 j + 1 ----
       float sc[2][4];
 #pragma unroll
@@ -538,7 +545,6 @@ kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
           for (int r = 0; r < 2; ++r) {
             const int t = h * 16 + r * 8 + g;
             sv[h][r] = __low2float(vp[t * NG + i]);
-            if (edge && !seen(t)) sv[h][r] = 0.f;
             top = fmaxf(top, fabsf(sv[h][r]));
           }
         int e2 = min((int)(__float_as_uint(top) >> 23) - 127, 15);     // top < 2^(e2 + 1)
@@ -565,19 +571,21 @@ kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
       for (int h = 0; h < 2; ++h) {
         const int ta = h * 16 + 2 * j;    // this lane's tokens: ta, ta + 1, ta + 8, ta + 9
         auto zeros = [&](int i, int t) {
-          __half2 p0 = vp[t * NG + i], p1 = vp[(t + 1) * NG + i];
-          const __half none = __ushort_as_half((unsigned short)0);
-          if (edge && !seen(t)) p0 = __half2half2(none);
-          if (edge && !seen(t + 1)) p1 = __half2half2(none);
-          return make_zero(__highs2half2(p0, p1));
+          return make_zero(__highs2half2(vp[t * NG + i], vp[(t + 1) * NG + i]));
         };
         auto word = [&](int t, int w) { return lds32(vc + piece<D>(t, w >> 2) + (w & 3) * 4); };
         if constexpr (GROUP >= 64) {
           // rows g and g + 8 of feature tile (f, i): nibbles i and i + 4 of word 8 f + g
+          Zero z0[NG], z1[NG];
+#pragma unroll
+          for (int i = 0; i < NG; ++i) {
+            z0[i] = zeros(i, ta);
+            z1[i] = zeros(i, ta + 8);
+          }
 #pragma unroll
           for (int f = 0; f < D / 64; ++f) {
             const int w = 8 * f + g, grp = f * 64 / GROUP;
-            const Zero za = zeros(grp, ta), zb = zeros(grp, ta + 8);
+            const Zero za = z0[grp], zb = z1[grp];
             const uint32_t wa = word(ta, w), wb = word(ta + 1, w), wc = word(ta + 8, w), wd = word(ta + 9, w);
             uint32_t x0 = __byte_perm(wa, wb, 0x5410), x1 = __byte_perm(wa, wb, 0x7632);
             uint32_t y0 = __byte_perm(wc, wd, 0x5410), y1 = __byte_perm(wc, wd, 0x7632);
