@@ -10,11 +10,13 @@
 // Sums are fp32; the layer norm takes its squares from the centred values (a second
 // pass over registers, not over memory), so a large mean costs no digits.
 //
-// Bound: HBM.  A row is read once into registers (16 values per thread up to d = 16384,
-// 32 above) and every statistic is taken there; x, y and the gate are read and xn and h
-// written once; the parameters come from L1 and are applied a row piece at a time, so that
-// x and y are all that a thread holds.  Rows of up to 512 values take one warp each (no
-// block barrier), longer rows one block.  Where rows do not start on 16-byte boundaries (an
+// Bound: HBM.  A row is read once into registers (8 values per thread up to d = 256, 16 up to
+// 4096, 32 above: fewer threads meet at the barriers, 4000 rows of 8192 with norms on both
+// sides 84 us with 16, 65 with 32) and every statistic is taken there; x, y and the gate are
+// read and xn and h written once; the parameters come from L1 and are applied a row piece at a
+// time, so that x and y are all that a thread holds.  Rows of up to 512 values take a warp each,
+// of up to 128 and 64 a half and a quarter of one (no block barrier; 200,000 rows of 64: 99 us
+// with a warp each, 32 so), longer rows a block.  Where rows do not start on 16-byte boundaries (an
 // odd d or stride) a thread of a 16-bit stream still takes eight consecutive values: it reads
 // the aligned 16-byte pieces that hold them and shifts, and writes by way of shared memory,
 // where each thread picks up what belongs to one aligned piece; single values only at a row's
@@ -48,6 +50,7 @@ struct NormArgs {
 };
 
 constexpr int ANY = -1;
+constexpr int LONG = 4096;                // values of a row above which a thread takes 32
 
 // A row's threads and their places.  T = 0: any number of threads with eight consecutive
 // values per piece, which lie on 16-byte boundaries; ANY: the same on any boundaries; else T
@@ -60,12 +63,16 @@ struct Row {
   }
 };
 
-// Sum over the row's threads (a warp, or the whole block through `part`, its own for each sum).
+// Sum over the row's threads (8, 16 or 32 of a warp, or the whole block through `part`, its own
+// for each sum).
 template <int T>
 __device__ __forceinline__ float row_sum(float v, float* part) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (Row<T>::threads() == 32) return v;
+  for (int o = 16; o > 0; o >>= 1) {
+    const float w = __shfl_xor_sync(0xffffffffu, v, o);
+    if (o < Row<T>::threads()) v += w;
+  }
+  if (Row<T>::threads() <= 32) return v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = Row<T>::threads() >> 5;
   if (lane == 0) part[warp] = v;
   __syncthreads();
@@ -178,9 +185,9 @@ __device__ __forceinline__ void apply(const void* p, int64_t off, int dtype, int
 
 // A row of 16-bit values to any boundary, by way of `buf` (16 bytes for each eight values).
 template <int V, typename S>
-__device__ __forceinline__ void store_any(S* row, int d, const float (&x)[V * 8], uint4* buf) {
+__device__ __forceinline__ void store_any(S* row, int d, const float (&x)[V * 8], uint4* buf, bool real) {
   const int n = (int)blockDim.x, pieces = (d + 7) / 8;
-  if (n == 32) __syncwarp();              // the last row's readers are done
+  if (n <= 32) __syncwarp();              // the last row's readers are done
   else __syncthreads();
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -188,11 +195,11 @@ __device__ __forceinline__ void store_any(S* row, int d, const float (&x)[V * 8]
     const int i = v * n + (int)threadIdx.x;
     if (i < pieces) buf[i] = make_uint4(pack2(y[0], y[1], S()), pack2(y[2], y[3], S()), pack2(y[4], y[5], S()), pack2(y[6], y[7], S()));
   }
-  if (n == 32) __syncwarp();
+  if (n <= 32) __syncwarp();
   else __syncthreads();
   const uint32_t mis = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
   const int off = (int)mis / 2;           // piece c of memory: values 8 c - off .. 8 c - off + 7
-  for (int c = (int)threadIdx.x; c * 8 - off < d; c += n) {
+  for (int c = (int)threadIdx.x; real && c * 8 - off < d; c += n) {
     const uint4 a = c > 0 ? buf[c - 1] : make_uint4(0, 0, 0, 0);
     const uint4 b = c < pieces ? buf[c] : make_uint4(0, 0, 0, 0);
     uint32_t w[8] = {b.x, b.y, b.z, b.w, 0, 0, 0, 0};
@@ -214,11 +221,12 @@ __device__ __forceinline__ void store_any(S* row, int d, const float (&x)[V * 8]
 }
 
 template <int V, int T, typename S>
-__device__ __forceinline__ void store_row(S* row, int d, const float (&x)[V * 8], uint4* buf) {
+__device__ __forceinline__ void store_row(S* row, int d, const float (&x)[V * 8], uint4* buf, bool real) {
   if constexpr (T == ANY) {
-    if constexpr (sizeof(S) == 2) store_any<V>(row, d, x, buf);
+    if constexpr (sizeof(S) == 2) store_any<V>(row, d, x, buf, real);
     return;
   }
+  if (!real) return;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     if constexpr (T == 0) {
@@ -255,17 +263,20 @@ __device__ __forceinline__ void norm_row(float (&x)[V * 8], const void* w, const
   if (b != nullptr) apply<V, T>(b, 0, A.p_dtype, A.d, x, [](float a, float p) { return a + p; });
 }
 
-// ROWS rows of a warp each (T 0, ANY or 32), or one row per block of up to MAXT threads (384:
-// three blocks to an SM, which hide each other's barriers; four would spill).
-template <typename TX, int V, int T, int ROWS, int MAXT>
+// Rows of blockDim.x threads: blockDim.y rows of part of a warp each (WARPS; T 0, ANY or 32), or
+// one row per block of up to MAXT threads (384: three blocks to an SM, which hide each other's
+// barriers; four would spill).
+template <typename TX, int V, int T, bool WARPS, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT == 384 ? 3 : 1024 / MAXT)
 add_norm_kernel(const NormArgs A, const int32_t* st) {
   __shared__ float part[4][32];
   extern __shared__ uint4 pieces[];       // ANY: 16 bytes for each eight values of the block's rows
-  uint4* buf = pieces + (int)threadIdx.y * 64;
+  uint4* buf = pieces + (int)threadIdx.y * (V * (int)blockDim.x);
   if (has_error(st)) return;
-  const int row = (int)blockIdx.x * ROWS + (int)threadIdx.y;
-  if (ROWS > 1 && row >= A.tokens) return;
+  int row = WARPS ? (int)(blockIdx.x * blockDim.y + threadIdx.y) : (int)blockIdx.x;
+  // a warp's last rows may be none: it goes through the last one again and writes nothing
+  const bool real = !WARPS || row < A.tokens;
+  if (WARPS) row = min(row, A.tokens - 1);
   const TX* X = static_cast<const TX*>(A.X) + (int64_t)row * A.ld_x;
   float y[V * 8];
   if (A.Y == nullptr) {
@@ -273,48 +284,56 @@ add_norm_kernel(const NormArgs A, const int32_t* st) {
   } else {
     float x[V * 8];
     typed(A.Y, (int64_t)row * A.ld_y, A.y_dtype, [&](auto* r) { load_row<V, T>(r, A.d, y); });
-    if constexpr (V == 2) load_row<V, T>(X, A.d, x);    // early; of 32 values only y is held through the norm
+    if constexpr (V <= 2) load_row<V, T>(X, A.d, x);    // early; of 32 values only y is held through the norm
     if (A.post_weight != nullptr) norm_row<V, T>(y, A.post_weight, A.post_bias, A, part);
     if (A.gate != nullptr)
       apply<V, T>(A.gate, (int64_t)row * A.ld_gate, A.p_dtype, A.d, y, [](float a, float g) { return a * g; });
-    if constexpr (V != 2) load_row<V, T>(X, A.d, x);
+    if constexpr (V > 2) load_row<V, T>(X, A.d, x);
 #pragma unroll
     for (int i = 0; i < V * 8; ++i) y[i] = round_to<TX>(fmaf(A.alpha, y[i], x[i]));
-    store_row<V, T>(static_cast<TX*>(A.Xn) + (int64_t)row * A.ld_xn, A.d, y, buf);
+    store_row<V, T>(static_cast<TX*>(A.Xn) + (int64_t)row * A.ld_xn, A.d, y, buf, real);
   }
   norm_row<V, T>(y, A.weight, A.bias, A, part + 2);
-  store_row<V, T>(static_cast<TX*>(A.h) + (int64_t)row * A.ld_h, A.d, y, buf);
+  store_row<V, T>(static_cast<TX*>(A.h) + (int64_t)row * A.ld_h, A.d, y, buf, real);
 }
 
 template <typename TX>
 void launch(const NormArgs& A, bool vec, const int32_t* st, cudaStream_t s) {
-  const unsigned rows8 = (unsigned)cdiv(A.tokens, 8), rows = (unsigned)A.tokens;
-  const dim3 warps(32, 8);
+  const unsigned rows = (unsigned)A.tokens;
+  // threads of a row that a warp holds; rows of a block of 256
+  const unsigned lanes = A.d <= 64 ? 8 : (A.d <= 128 ? 16 : 32);
+  const dim3 warps(lanes, 256 / lanes);
+  const unsigned groups = (unsigned)cdiv(A.tokens, 256 / lanes);
   if (vec) {
-    const unsigned thr = (unsigned)(cdiv(cdiv(A.d, A.d <= 16384 ? 16 : 32), 32) * 32);
-    if (A.d <= 512) add_norm_kernel<TX, 2, 0, 8, 256><<<rows8, warps, 0, s>>>(A, st);
-    else if (A.d <= 16384) add_norm_kernel<TX, 2, 0, 1, 1024><<<rows, thr, 0, s>>>(A, st);
-    else add_norm_kernel<TX, 4, 0, 1, 1024><<<rows, thr, 0, s>>>(A, st);
+    const unsigned thr = (unsigned)(cdiv(cdiv(A.d, A.d <= LONG ? 16 : 32), 32) * 32);
+    if (A.d <= 256) add_norm_kernel<TX, 1, 0, true, 256><<<groups, warps, 0, s>>>(A, st);
+    else if (A.d <= 512) add_norm_kernel<TX, 2, 0, true, 256><<<groups, warps, 0, s>>>(A, st);
+    else if (A.d <= LONG) add_norm_kernel<TX, 2, 0, false, 1024><<<rows, thr, 0, s>>>(A, st);
+    else add_norm_kernel<TX, 4, 0, false, 1024><<<rows, thr, 0, s>>>(A, st);
     return;
   }
   if constexpr (sizeof(TX) == 2) {
-    if (A.d <= 512) add_norm_kernel<TX, 2, ANY, 8, 256><<<rows8, warps, 8 * 64 * 16, s>>>(A, st);
+    if (A.d <= 256) add_norm_kernel<TX, 1, ANY, true, 256><<<groups, warps, 256 * 16, s>>>(A, st);
+    else if (A.d <= 512) add_norm_kernel<TX, 2, ANY, true, 256><<<groups, warps, 512 * 16, s>>>(A, st);
     else if (A.d <= 16384) {
       const unsigned thr = (unsigned)(cdiv(cdiv(A.d, 16), 32) * 32);
-      const size_t smem = (size_t)cdiv(A.d, 8) * 16;
-      if (thr <= 384) add_norm_kernel<TX, 2, ANY, 1, 384><<<rows, thr, smem, s>>>(A, st);
-      else add_norm_kernel<TX, 2, ANY, 1, 1024><<<rows, thr, smem, s>>>(A, st);
+      const size_t smem = (size_t)thr * 2 * 16;
+      if (thr <= 384) add_norm_kernel<TX, 2, ANY, false, 384><<<rows, thr, smem, s>>>(A, st);
+      else add_norm_kernel<TX, 2, ANY, false, 1024><<<rows, thr, smem, s>>>(A, st);
     } else {
-      add_norm_kernel<TX, 4, 1024, 1, 1024><<<rows, 1024, 0, s>>>(A, st);
+      add_norm_kernel<TX, 4, 1024, false, 1024><<<rows, 1024, 0, s>>>(A, st);
     }
   } else {
-    if (A.d <= 512) add_norm_kernel<TX, 2, 32, 8, 256><<<rows8, warps, 0, s>>>(A, st);
-    else if (A.d <= 1024) add_norm_kernel<TX, 2, 64, 1, 64><<<rows, 64, 0, s>>>(A, st);
-    else if (A.d <= 2048) add_norm_kernel<TX, 2, 128, 1, 128><<<rows, 128, 0, s>>>(A, st);
-    else if (A.d <= 4096) add_norm_kernel<TX, 2, 256, 1, 256><<<rows, 256, 0, s>>>(A, st);
-    else if (A.d <= 8192) add_norm_kernel<TX, 2, 512, 1, 512><<<rows, 512, 0, s>>>(A, st);
-    else if (A.d <= 16384) add_norm_kernel<TX, 2, 1024, 1, 1024><<<rows, 1024, 0, s>>>(A, st);
-    else add_norm_kernel<TX, 4, 1024, 1, 1024><<<rows, 1024, 0, s>>>(A, st);
+    const dim3 warp32(32, 8);
+    const unsigned groups32 = (unsigned)cdiv(A.tokens, 8);
+    if (A.d <= 256) add_norm_kernel<TX, 1, 32, true, 256><<<groups32, warp32, 0, s>>>(A, st);
+    else if (A.d <= 512) add_norm_kernel<TX, 2, 32, true, 256><<<groups32, warp32, 0, s>>>(A, st);
+    else if (A.d <= 1024) add_norm_kernel<TX, 2, 64, false, 64><<<rows, 64, 0, s>>>(A, st);
+    else if (A.d <= 2048) add_norm_kernel<TX, 2, 128, false, 128><<<rows, 128, 0, s>>>(A, st);
+    else if (A.d <= 4096) add_norm_kernel<TX, 2, 256, false, 256><<<rows, 256, 0, s>>>(A, st);
+    else if (A.d <= 8192) add_norm_kernel<TX, 2, 512, false, 512><<<rows, 512, 0, s>>>(A, st);
+    else if (A.d <= 16384) add_norm_kernel<TX, 2, 1024, false, 1024><<<rows, 1024, 0, s>>>(A, st);
+    else add_norm_kernel<TX, 4, 1024, false, 1024><<<rows, 1024, 0, s>>>(A, st);
   }
 }
 
