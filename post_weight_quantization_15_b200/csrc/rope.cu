@@ -10,9 +10,12 @@
 // Bound: HBM (4 bytes in, 2 out per value).  One pass.  A thread keeps the same W pairs of
 // every head it takes, so that their cosines and sines are read once into registers and a
 // head costs two 16-byte loads (W = 4 of fp32, 8 of 16-bit types, side by side across a
-// warp) and two stores; W = 1 for any even rot and any alignment.  A block stays within one
-// token.  (A unit of 16 values per thread with the tables read again for every head took
-// 190 us for 8192 tokens of 96 heads x 128 where this one takes 117.)
+// warp) and two stores; W = 1 for any even rot and any alignment.  Where there are tokens
+// enough, a thread takes four heads or more and a block as many tokens as its threads hold.
+// 8192 tokens of 96 heads x 128, fp32 in, bias: 190 us with 16 values per thread and the tables
+// read again for every head, 117 so, 111 with two heads in flight instead of four and five
+// blocks per SM (84% of the copy bandwidth); 89,731 tokens of 6 heads: 227 us with one token
+// per block, 80 with eight.
 #include "common.cuh"
 #include "internal.h"
 #include "vec_io.cuh"
@@ -51,20 +54,21 @@ __device__ __forceinline__ void storew(T* p, const float (&v)[W]) {
   else store_from_float(p, v[0]);
 }
 
-// Thread: pairs j W .. j W + W - 1 of heads h0, h0 + step, ...; a head has `units` = d / (2 W)
-// such pieces (W = 1: rot and d even), the first rot / (2 W) of them rotated in q and k heads.
+// Thread: pairs j W .. j W + W - 1 of heads h0, h0 + subs, ... of one token; a head has `units` =
+// d / (2 W) such pieces (W = 1: rot and d even), the first rot / (2 W) of them rotated in q and k
+// heads.  A block has `per` tokens of subs . units threads, or (per 1) a part of one token's heads.
 template <typename TX, typename TO, int W, bool BIAS>
-__global__ void __launch_bounds__(THREADS)
-rope_qkv_kernel(const __grid_constant__ RopeArgs A, int units, int per_block, int32_t* st) {
+__global__ void __launch_bounds__(THREADS, W == 8 ? 4 : 5)
+rope_qkv_kernel(const __grid_constant__ RopeArgs A, int units, int subs, int per, int per_block, int32_t* st) {
   if (has_error(st)) return;
-  const int t = (int)blockIdx.x;
   const int turned = A.hq + A.hk, heads = turned + A.hk;
-  const int sub = (int)threadIdx.x / units, subs = max(1, min(THREADS / units, per_block));
+  const int sub = (int)threadIdx.x / units % subs, own = (int)threadIdx.x / (units * subs);
+  const int t = (int)blockIdx.x * per + own;
   const int begin = (int)blockIdx.y * per_block, end = min(heads, begin + per_block);
-  if (sub >= subs) return;
+  if (own >= per || t >= A.tokens) return;
   int pos = A.positions != nullptr ? A.positions[t] : t;
   if (A.rot > 0 && (pos < 0 || pos >= A.max_pos)) {
-    if (threadIdx.x == 0 && blockIdx.y == 0) set_error(st, GPTQ_ERR_INVALID_ARG, t, STAGE_ROPE);
+    if (threadIdx.x % (units * subs) == 0 && blockIdx.y == 0) set_error(st, GPTQ_ERR_INVALID_ARG, t, STAGE_ROPE);
     pos = 0;
   }
   for (int j = (int)threadIdx.x % units; j < units; j += THREADS) {      // units above the block's threads: W = 1 only
@@ -79,7 +83,7 @@ rope_qkv_kernel(const __grid_constant__ RopeArgs A, int units, int per_block, in
       loadw<W>(A.sin + (int64_t)pos * (A.rot / 2) + j * W, s);
     }
     const TX* row = static_cast<const TX*>(A.X) + (int64_t)t * A.ld;
-#pragma unroll 4
+#pragma unroll 2
     for (int head = begin + sub; head < end; head += subs) {
       const int c0 = head * A.d + i0, c1 = head * A.d + i1;
       float a[W], b[W];
@@ -131,14 +135,18 @@ rope_qkv_kernel(const __grid_constant__ RopeArgs A, int units, int per_block, in
 template <typename TX, typename TO, int W>
 void launch_w(const RopeArgs& A, int32_t* st, cudaStream_t s) {
   const int units = A.d / (2 * W), heads = A.hq + 2 * A.hk;
-  const int subs = THREADS / units > 0 ? THREADS / units : 1;
-  // few tokens: a head per thread; else one block per token
+  const int most = THREADS / units > 0 ? THREADS / units : 1;
+  // many tokens: four heads or more per thread, several tokens per block; few: a head per thread
+  const bool many = (int64_t)A.tokens * units * heads >= (int64_t)ENOUGH * THREADS * 4;
+  const int quarter = (heads + 3) / 4;
+  int subs = many ? (quarter < most ? quarter : most) : (heads < most ? heads : most);
+  const int per = many && units <= THREADS ? THREADS / (units * subs) : 1;
   const int64_t want = cdiv(heads, subs);
-  const int64_t split = A.tokens >= ENOUGH ? 1 : (want < 64 ? want : 64);
+  const int64_t split = many ? 1 : (want < 64 ? want : 64);
   const int per_block = (int)cdiv(heads, split);
-  const dim3 grd((unsigned)A.tokens, (unsigned)cdiv(heads, per_block));
-  if (A.bias != nullptr) rope_qkv_kernel<TX, TO, W, true><<<grd, THREADS, 0, s>>>(A, units, per_block, st);
-  else rope_qkv_kernel<TX, TO, W, false><<<grd, THREADS, 0, s>>>(A, units, per_block, st);
+  const dim3 grd((unsigned)cdiv(A.tokens, per), (unsigned)cdiv(heads, per_block));
+  if (A.bias != nullptr) rope_qkv_kernel<TX, TO, W, true><<<grd, THREADS, 0, s>>>(A, units, subs, per, per_block, st);
+  else rope_qkv_kernel<TX, TO, W, false><<<grd, THREADS, 0, s>>>(A, units, subs, per, per_block, st);
 }
 
 template <typename TX, typename TO>
