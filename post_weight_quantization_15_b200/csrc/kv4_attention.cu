@@ -31,6 +31,15 @@
 // warp's run is joined in the block first, and the blocks' and the last warp's (maximum,
 // sum, weighted values) are left in the workspace, where kv4_join_kernel, a dependent
 // launch, joins them in a fixed order.
+//
+// 131,071 tokens x 64/8 heads of 128, groups of 128: 51 us with cold caches, 21.8 at the copy
+// bandwidth; 16 ragged sequences x 32 heads, groups of 32: 74 and 27.7.  (A block per query
+// head and token after token: 68.8 and 2.41 ms; rows padded to 16 heads, TMA rings and joins
+// per head set in the block: 100 and 620 us; cache as rows: 67 and 332; a run per warp: 65 and
+// 104; one lop3 per masked pair: 57 and 82; zero points once per half tile: 51 and 74.)  What
+// bounds it: instructions, 640 per tile of 32 tokens, 350 of them unpacking and products, at
+// 59 to 63% of the issue slots with the 16 warps per SM that 128 registers allow (20 warps
+// spill: 65 and 92 us; three stages per ring: 55 and 90).
 #include <math.h>
 
 #include <climits>
@@ -49,7 +58,6 @@ constexpr int PER_SM = 4;
 constexpr int BLOCKS = 148 * PER_SM;      // resident blocks: the cut of the work, whatever the device
 constexpr int WARPS = 4;
 constexpr int RUNS = BLOCKS * WARPS;
-constexpr int SHORTEST = 4;               // slots of a run, where there are few
 constexpr int TT = 32;                    // tokens of a tile
 constexpr int STAGES = 2;
 constexpr int ROWS = 8;                   // query heads of a product
@@ -142,10 +150,8 @@ __device__ __forceinline__ int run_of(int64_t all, int runs, int64_t slot) {
   while (c + 1 < runs && run_begin(all, runs, c + 1) <= slot) ++c;
   return c;
 }
-__device__ __forceinline__ int runs_of(int64_t all) {
-  const int64_t n = all < SHORTEST ? 1 : all / SHORTEST;
-  return (int)(n < RUNS ? n : RUNS);
-}
+// Down to one slot each: 300 tokens x 32/8 heads take 11 us, in runs of at least four 14.
+__device__ __forceinline__ int runs_of(int64_t all) { return (int)(all < RUNS ? (all > 0 ? all : 1) : RUNS); }
 
 template <int D, int GROUP>
 struct KvaSmem {
