@@ -228,13 +228,13 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // Slot `slot` (the sequences in order, a sequence's pairs from the last, which sees the most
-// keys, to the first) of head h; whole warp.  Sequences with bad bounds have no pairs and are
-// recorded.
-__device__ __forceinline__ Work find_work(const AttentionArgs& A, int slot, int h, int32_t* st) {
+// keys, to the first) of head h; whole warp.  The slots of one warp's calls ascend: b0 and base
+// (0 at first) say where the last one was found.  Sequences with bad bounds have no pairs and
+// are recorded.
+__device__ __forceinline__ Work find_work(const AttentionArgs& A, int slot, int h, int& b0, int& base, int32_t* st) {
   const int lane = threadIdx.x & 31;
   Work w{-1, h, 0, 0, 0, 0};
-  int base = 0;
-  for (int b0 = 0; b0 < A.count; b0 += 32) {
+  for (; b0 < A.count; b0 += 32) {
     const int b = b0 + lane;
     int pairs = 0, q0 = 0, q1 = 0, k0 = 0, k1 = 0;
     if (b < A.count) {
@@ -462,7 +462,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
   Work w{-1, 0, 0, 0, 0, 0};
 
   if (warp == 9) tc::tmem_alloc<512>(&S.tmem_base);
-  if (warp == 8) w = find_work(A, at / A.heads_q, at % A.heads_q, at % A.heads_q == 0 && rank == 0 ? st : nullptr);
+  int b0 = 0, base = 0;
+  if (warp == 8) w = find_work(A, at / A.heads_q, at % A.heads_q, b0, base, st);
   if (warp == 0 && lane == 0) {
     S.skip = has_error(st);
     S.abort = 0;
@@ -543,7 +544,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
         at += step;
         w.pair = -1;
         if (!SPLIT && at < pairs)
-          w = find_work(A, at / A.heads_q, at % A.heads_q, at % A.heads_q == 0 ? st : nullptr);
+          w = find_work(A, at / A.heads_q, at % A.heads_q, b0, base, st);
       }
     } else if (warp == 9) {
       // The whole warp walks the loop, so that the products' descriptors stay in uniform

@@ -71,7 +71,7 @@ rope_qkv_kernel(const __grid_constant__ RopeArgs A, int units, int subs, int per
     if (threadIdx.x % (units * subs) == 0 && blockIdx.y == 0) set_error(st, GPTQ_ERR_INVALID_ARG, t, STAGE_ROPE);
     pos = 0;
   }
-  for (int j = (int)threadIdx.x % units; j < units; j += THREADS) {      // units above the block's threads: W = 1 only
+  for (int j = (int)threadIdx.x % units; j < units; j += THREADS) {      // (a head may have more pieces than the block threads)
     const bool turn = j * 2 * W < A.rot;
     // the piece's two runs of W values inside a head
     const bool split = turn && !A.interleaved;

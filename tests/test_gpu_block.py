@@ -165,6 +165,9 @@ ROPE_CASES = [
     (2, 5, 1, 36, 12, FF, HF, True, True, True),
     (2, 5, 1, 36, 36, FF, BF, False, False, True),
     (2, 40, 8, 128, 0, FF, BF, False, True, False),
+    (6401, 4, 1, 128, 128, FF, BF, False, True, True),       # several tokens per block
+    (15203, 2, 1, 80, 40, BF, HF, True, True, True),
+    (2, 1, 1, 4096, 4096, FF, BF, False, True, True),        # a head wider than a block
 ]
 
 
@@ -345,6 +348,18 @@ def test_attention_many_pairs_per_block(hq, hk, d, dt, causal):
     past = [max(p, -n) for p, n in zip(past, lens)]
     past[10] = -lens[10]                                     # a sequence without keys
     test_attention(lens, past, hq, hk, d, dt, causal)
+
+
+def test_attention_very_many_sequences():
+    rng = np.random.default_rng(77)
+    lens = [int(n) for n in rng.integers(0, 4, 3000)]
+    test_attention(lens, [int(n) for n in rng.integers(0, 3, 3000)], 2, 1, 64, HF, True)
+    q, k, v, cq, ck = _attn_inputs([1] * 2000, [0] * 2000, 3, 1, 64, HF)
+    cq[1500] = -5                                            # sequences 1499 and 1500 have bad bounds
+    st = G.new_status(q.device)
+    G.attention(q, k, v, _int(cq), _int(ck), status=st)
+    code, at = G.status_read(st)
+    assert code == G.gptq.ERR_INVALID_ARG and at in (1499, 1500)
 
 
 def test_attention_large_scores_and_scale():
