@@ -135,6 +135,31 @@ def test_add_norm_strided_rows_and_neighbours():
         assert (out[:, 256:] == 7).all() and (xo[:, 256:] == 7).all()
 
 
+@pytest.mark.parametrize("xt,yt", [(BF, HF), (HF, FF), (FF, BF)])
+@pytest.mark.parametrize("d", [1, 3, 8, 61, 64, 100, 129, 256, 260, 513, 4099])
+def test_add_norm_from_any_address(d, xt, yt):
+    """Rows that start on every element of a 16-byte piece give what aligned rows give, and write nothing else."""
+    rng = np.random.default_rng(d)
+    t = 11
+    X, Y, w = _rand(rng, (t, d), xt), _rand(rng, (t, d), yt), _rand(rng, (d + 3,), xt)[3:]
+    want, _ = G.add_norm(X, w.clone(), Y=Y, post_weight=w.clone(), center=d > 1, eps=1e-3)
+    for shift in (1, 2, 5, 7):
+        def at(src):
+            flat = torch.full((t * d + 16,), 7.0, dtype=src.dtype, device=src.device)
+            flat[shift:shift + t * d] = src.flatten()
+            return flat, flat[shift:shift + t * d].view(t, d)
+        (_, Xs), (_, Ys), (fx, xo), (fo, ho) = at(X), at(Y), at(torch.zeros_like(X)), at(torch.zeros_like(X))
+        G.add_norm(Xs, w, Y=Ys, post_weight=w, center=d > 1, eps=1e-3, x_out=xo, out=ho)
+        for f in (fx, fo):
+            assert (f[:shift] == 7).all() and (f[shift + t * d:] == 7).all()
+        # either side's normed Y is within the bound of itself and rounded once with X; h likewise, from the same Xn
+        _, mag, _ = _norm_tol(_np(Y), _np(w), None, 1e-3, d > 1, FF)
+        r = _np(want)
+        _close(xo, r, 2 * (mag + 4 * W * (np.abs(_np(X)) + np.abs(r)) + U[xt] * np.abs(r) + TINY[xt]) * (1 + U[xt]), shift)
+        hr, _, ht = _norm_tol(_np(xo), _np(w), None, 1e-3, d > 1, xt)
+        _close(ho, hr, ht, shift)
+
+
 def test_add_norm_extreme_rows():
     """A row of zeros gives the bias; a large common mean costs the layer norm no digits; NaN stays in its row."""
     d = 640
@@ -608,6 +633,44 @@ def test_kv4_attention_nan_stays_in_its_rows(n):
     assert torch.isnan(got[0, 4:, 64:]).all()
     got[0, 4:, 64:] = clean[0, 4:, 64:]
     assert torch.equal(got, clean)
+
+
+def test_kv4_attention_very_many_sequences():
+    rng = np.random.default_rng(12)
+    lens = [int(n) for n in rng.integers(0, 4, 3000)]
+    cache, table, k64, v64 = _kv_cache(rng, lens, 1, 64, 32, 16, HF)
+    q = _rand(rng, (3000, 2, 64), HF)
+    o = G.kv4_attention(q, cache, table, _int(lens))
+    ref, tol = _attn_tol(_np(q), k64, v64, list(range(3001)), _cu(lens), 0.125, False, HF, 2.0 ** -11, dq=2.0 ** -25,
+                         small=2.0 ** -33)
+    _close(o, ref, tol, "o")
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Long calls of every operator on two streams at the same time give what they give alone."""
+    rng = np.random.default_rng(13)
+    lens = [[20000, 300], [15000, 7000]]
+    made = [_kv_cache(rng, ln, 4, 128, 64, 64, BF)[:2] for ln in lens]
+    qs = [_rand(rng, (2, 16, 128), BF) for _ in lens]
+    qkv = [[_rand(rng, (1500, h, 128), BF) for h in (16, 4, 4)] for _ in lens]
+    cu = _int([0, 400, 1500])
+    X = [_rand(rng, (3000, 1000), HF) for _ in lens]
+    w = _rand(rng, (1000,), HF)
+
+    def go(i):
+        return (G.kv4_attention(qs[i], made[i][0], made[i][1], _int(lens[i])), G.attention(*qkv[i], cu),
+                *G.add_norm(X[i], w, Y=X[1 - i]))
+    want = [go(0), go(1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in lens]
+    for _ in range(5):
+        got = []
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got.append(go(i))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
 def test_kv4_attention_records_bad_lengths_and_pages():
