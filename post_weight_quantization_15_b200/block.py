@@ -204,11 +204,12 @@ def rope_qkv(QKV: torch.Tensor, cos: Optional[torch.Tensor], sin: Optional[torch
         raise ValueError("cos and sin go together")
     rot = max_pos = 0
     if cos is not None:
-        for t in (cos, sin):
-            if t.dtype != torch.float32 or t.dim() != 2 or t.shape != cos.shape or not t.is_contiguous():
-                raise ValueError("cos and sin must be contiguous fp32 [positions, rot / 2] tensors of one shape")
-        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
-    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (cols,) or not bias.is_contiguous()):
+        if cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.dim() != 2 or sin.shape != cos.shape \
+                or not cos.is_contiguous() or not sin.is_contiguous():
+            raise ValueError("cos and sin must be contiguous fp32 [positions, rot / 2] tensors of one shape")
+        max_pos, half = cos.shape
+        rot = 2 * half
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (cols,) or not bias.is_contiguous()):
         raise ValueError(f"bias must be a contiguous fp32 [{cols}] tensor")
     if positions is not None:
         _ints(positions, (tokens,), "positions")
@@ -217,10 +218,12 @@ def rope_qkv(QKV: torch.Tensor, cos: Optional[torch.Tensor], sin: Optional[torch
         q = QKV.new_empty((tokens, heads_q, head_dim), dtype=dtype)
         k = QKV.new_empty((tokens, heads_kv, head_dim), dtype=dtype)
         v = torch.empty_like(k)
-        _check(lib().gptq_rope_qkv(_at(QKV), _DTYPE_CODE[QKV.dtype], _ld(QKV, cols), _at(bias), _at(cos),
-                                   _at(sin), max_pos, rot, int(bool(interleaved)), _at(positions), tokens, heads_q,
-                                   heads_kv, head_dim, _DTYPE_CODE[dtype], _at(q), _at(k), _at(v), _at(status),
-                                   s), "gptq_rope_qkv")
+        rc = lib().gptq_rope_qkv(QKV.data_ptr(), _DTYPE_CODE[QKV.dtype], cols if tokens <= 1 else QKV.stride(0),
+                                 _at(bias), _at(cos), _at(sin), max_pos, rot, bool(interleaved), _at(positions),
+                                 tokens, heads_q, heads_kv, head_dim, _DTYPE_CODE[dtype], q.data_ptr(), k.data_ptr(),
+                                 v.data_ptr(), _at(status), s)
+    if rc != OK:
+        raise GptqError(rc, "gptq_rope_qkv")
     return q, k, v
 
 
@@ -228,17 +231,15 @@ def rope_qkv(QKV: torch.Tensor, cos: Optional[torch.Tensor], sin: Optional[torch
 # Attention over packed prompts
 # --------------------------------------------------------------------------- #
 def _heads(t: torch.Tensor, dtype, what: str):
-    if t.dim() != 3 or t.dtype != dtype or t.shape[1] < 1 or (t.shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError(f"{what} must be a [tokens, heads, head_dim] tensor of type {dtype} with contiguous features")
-
-
-def _strides(t: torch.Tensor):
-    """Token and head strides; those of a single token or head are not used."""
-    n, h, d = t.shape
-    ts, hs, _ = t.stride()
-    if h == 1:
-        hs = d
-    return (ts if n > 1 else h * hs), hs
+    """(tokens, heads, head_dim, token stride, head stride); strides of a single token or head are not used."""
+    if t.dim() == 3 and t.dtype == dtype:
+        n, h, d = t.shape
+        ts, hs, fs = t.stride()
+        if h > 0 and (fs == 1 or d <= 1):
+            if h == 1:
+                hs = d
+            return n, h, d, ts if n > 1 else h * hs, hs
+    raise ValueError(f"{what} must be a [tokens, heads, head_dim] tensor of type {dtype} with contiguous features")
 
 
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
@@ -251,32 +252,37 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Ten
     causal: the last query of a sequence sees its last key.  scale None: 1 / sqrt(head_dim).
     Rows of o that belong to no sequence are not written.
     """
-    if q.dtype not in _16BIT:
+    dt = q.dtype
+    if dt not in _16BIT:
         raise ValueError("q must be fp16 or bf16")
-    for t, what in ((q, "q"), (k, "k"), (v, "v")):
-        _heads(t, q.dtype, what)
-    hq, d = q.shape[1], q.shape[2]
-    hk = k.shape[1]
-    if k.shape != v.shape or k.shape[2] != d or hq % hk != 0:
+    nq, hq, d, qt, qh = _heads(q, dt, "q")
+    nk, hk, dk, kt, kh = _heads(k, dt, "k")
+    nv, hv, dv, vt, vh = _heads(v, dt, "v")
+    if nk != nv or hk != hv or dk != d or dv != d or hq % hk != 0:
         raise ValueError("k and v must have one shape, q's head size, and a number of heads that divides q's")
-    cu_k = cu_q if cu_k is None else cu_k
+    if cu_k is None:
+        cu_k = cu_q
     if cu_q.dim() != 1 or cu_q.numel() < 1:
         raise ValueError("cu_q must be int32 [sequences + 1]")
     _ints(cu_q, cu_q.shape, "cu_q")
-    _ints(cu_k, cu_q.shape, "cu_k")
+    if cu_k is not cu_q:
+        _ints(cu_k, cu_q.shape, "cu_k")
     _status_ok(status)
     with _Launching(stream, q, k, v, cu_q, cu_k, out, status) as s:
         if out is None:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            ot, oh = hq * d, d
         else:
-            _heads(out, q.dtype, "out")
+            _, _, _, ot, oh = _heads(out, dt, "out")
             if out.shape != q.shape:
                 raise ValueError("out must have q's shape")
             _apart(out, q, k, v)
-        _check(lib().gptq_attention(_at(q), *_strides(q), _at(k), *_strides(k), _at(v), *_strides(v),
-                                    _DTYPE_CODE[q.dtype], _at(cu_q), _at(cu_k), cu_q.numel() - 1, q.shape[0],
-                                    k.shape[0], hq, hk, d, float(d ** -0.5 if scale is None else scale),
-                                    int(bool(causal)), _at(out), *_strides(out), _at(status), s), "gptq_attention")
+        rc = lib().gptq_attention(q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, _DTYPE_CODE[dt],
+                                  cu_q.data_ptr(), cu_k.data_ptr(), cu_q.numel() - 1, nq, nk, hq, hk, d,
+                                  d ** -0.5 if scale is None else float(scale), bool(causal), out.data_ptr(), ot, oh,
+                                  _at(status), s)
+    if rc != OK:
+        raise GptqError(rc, "gptq_attention")
     return out
 
 
@@ -301,26 +307,26 @@ def kv4_alloc(pages: int, page_size: int, heads: int, head_dim: int, group: int 
 
 
 def _cache(c: KV4Cache) -> _KV4:
-    if c.k_codes.dim() != 4:
+    kc, kp, vc, vp, group = c.k_codes, c.k_params, c.v_codes, c.v_params, c.group
+    if kc.dim() != 4:
         raise ValueError("k_codes must be int32 [pages, heads, page_size, head_dim / 8]")
-    pages, heads, page, words = c.k_codes.shape
+    shape = kc.shape
+    pages, heads, page, words = shape
     d = words * 8
-    if c.group < 1 or d % c.group:
+    if group < 1 or d % group:
         raise ValueError("group must divide head_dim")
-    shape, pshape = c.k_codes.shape, (pages, heads, page, d // c.group, 2)
-    for codes, par in ((c.k_codes, c.k_params), (c.v_codes, c.v_params)):
-        if codes.dtype != torch.int32 or codes.shape != shape or not codes.is_contiguous():
-            raise ValueError("codes must be contiguous int32 tensors of one shape")
-        if par.dtype != torch.float16 or par.shape != pshape or not par.is_contiguous():
-            raise ValueError("params must be contiguous fp16 [pages, heads, page_size, head_dim / group, 2] tensors")
-    return _KV4(c.k_codes.data_ptr(), c.k_params.data_ptr(), c.v_codes.data_ptr(), c.v_params.data_ptr(), pages, page,
-                heads, d, int(c.group))
+    i32, f16 = torch.int32, torch.float16
+    if kc.dtype != i32 or vc.dtype != i32 or vc.shape != shape or not kc.is_contiguous() or not vc.is_contiguous():
+        raise ValueError("codes must be contiguous int32 tensors of one shape")
+    if kp.dtype != f16 or vp.dtype != f16 or kp.shape != (pages, heads, page, d // group, 2) or vp.shape != kp.shape \
+            or not kp.is_contiguous() or not vp.is_contiguous():
+        raise ValueError("params must be contiguous fp16 [pages, heads, page_size, head_dim / group, 2] tensors")
+    return _KV4(kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), pages, page, heads, d, int(group))
 
 
 def _table(table: torch.Tensor, count: int):
-    if table.dim() != 2 or table.shape[0] != count:
-        raise ValueError("table must be int32 [sequences, pages of a sequence]")
-    _ints(table, table.shape, "table")
+    if table.dim() != 2 or table.dtype != torch.int32 or table.shape[0] != count or not table.is_contiguous():
+        raise ValueError("table must be a contiguous int32 tensor [sequences, pages of a sequence]")
 
 
 def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, cu: torch.Tensor,
@@ -332,11 +338,12 @@ def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, table: torch.T
     [sequences + 1], start int32 [sequences].  A position must be written by one token only.
     """
     desc = _cache(cache)
-    if k.dtype not in _16BIT:
+    dt = k.dtype
+    if dt not in _16BIT:
         raise ValueError("k must be fp16 or bf16")
-    for t, what in ((k, "k"), (v, "v")):
-        _heads(t, k.dtype, what)
-    if k.shape != v.shape or k.shape[1] != desc.heads or k.shape[2] != desc.head_dim:
+    n, h, d, kt, kh = _heads(k, dt, "k")
+    nv, hv, dv, vt, vh = _heads(v, dt, "v")
+    if n != nv or h != hv or d != dv or h != desc.heads or d != desc.head_dim:
         raise ValueError("k and v must be [tokens, heads, head_dim] with the cache's heads and head_dim")
     count = start.numel()
     _ints(start, (count,), "start")
@@ -345,9 +352,11 @@ def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, table: torch.T
     _status_ok(status)
     with _Launching(stream, cache.k_codes, cache.k_params, cache.v_codes, cache.v_params, k, v, table, cu, start,
                     status) as s:
-        _check(lib().gptq_kv4_append(ctypes.byref(desc), _at(k), *_strides(k), _at(v), *_strides(v),
-                                     _DTYPE_CODE[k.dtype], k.shape[0], _at(table), table.shape[1], _at(cu),
-                                     _at(start), count, _at(status), s), "gptq_kv4_append")
+        rc = lib().gptq_kv4_append(ctypes.byref(desc), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, _DTYPE_CODE[dt], n,
+                                   table.data_ptr(), table.shape[1], cu.data_ptr(), start.data_ptr(), count,
+                                   _at(status), s)
+    if rc != OK:
+        raise GptqError(rc, "gptq_kv4_append")
     return cache
 
 
@@ -387,32 +396,38 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, table: torch.Tensor, lengths
                   out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
                   stream=None) -> torch.Tensor:
     """o [sequences, heads_q, head_dim]: one query token per sequence against positions
-    0 .. lengths[b] - 1 of its cache (lengths int32 [sequences]; 0 gives a row of 0)."""
+    0 .. lengths[b] - 1 of its cache (lengths int32 [sequences]; 0 gives a row of 0).
+
+    ws: at least kv4_attention_workspace_size(...) bytes (None: allocated for the call); calls that
+    may run at the same time need one each."""
     desc = _cache(cache)
-    if q.dtype not in _16BIT:
+    dt = q.dtype
+    if dt not in _16BIT:
         raise ValueError("q must be fp16 or bf16")
-    _heads(q, q.dtype, "q")
-    count, hq, d = q.shape
+    count, hq, d, qt, qh = _heads(q, dt, "q")
     if d != desc.head_dim or hq % desc.heads != 0:
         raise ValueError("q must have the cache's head size and a multiple of its heads")
     _ints(lengths, (count,), "lengths")
     _table(table, count)
     _status_ok(status)
+    width = table.shape[1]
     with _Launching(stream, cache.k_codes, cache.k_params, cache.v_codes, cache.v_params, q, table, lengths, ws, out,
                     status) as s:
-        need = kv4_attention_workspace_size(count, hq, desc.heads, d, table.shape[1], desc.page_size)
-        if ws is None or ws.numel() * ws.element_size() < need:
-            ws = workspace(need, q.device)
+        if ws is None:
+            ws = workspace(lib().gptq_kv4_attention_workspace_size(count, hq, desc.heads, d, width, desc.page_size),
+                           q.device)
         if out is None:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            ot, oh = hq * d, d
         else:
-            _heads(out, q.dtype, "out")
+            _, _, _, ot, oh = _heads(out, dt, "out")
             if out.shape != q.shape:
                 raise ValueError("out must have q's shape")
             _apart(out, q)
-        _check(lib().gptq_kv4_attention(ctypes.byref(desc), _at(q), *_strides(q), _DTYPE_CODE[q.dtype], count, hq,
-                                        _at(table), table.shape[1], _at(lengths),
-                                        float(d ** -0.5 if scale is None else scale), _at(out), *_strides(out),
-                                        _at(ws), ws.numel() * ws.element_size(), _at(status), s),
-               "gptq_kv4_attention")
+        rc = lib().gptq_kv4_attention(ctypes.byref(desc), q.data_ptr(), qt, qh, _DTYPE_CODE[dt], count, hq,
+                                      table.data_ptr(), width, lengths.data_ptr(),
+                                      d ** -0.5 if scale is None else float(scale), out.data_ptr(), ot, oh,
+                                      ws.data_ptr(), ws.numel() * ws.element_size(), _at(status), s)
+    if rc != OK:
+        raise GptqError(rc, "gptq_kv4_attention")
     return out
