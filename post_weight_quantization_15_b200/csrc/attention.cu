@@ -27,17 +27,21 @@
 // 16 x 2048 causal tokens x 32 heads of 128: 795 us with waits polled by one lane of a warp and
 // passed on, 730 polled by all lanes, 700 with the products issued by one elected thread, 680
 // with the weights handed over in two parts, 615 with blocks that stay (895 TFLOP/s); packed
-// sequences up to 6007, 64/8 heads: 1245, 1126, 1074, 1040, 1005 us (992 TFLOP/s).  What bounds
-// it: the chain of one tile, about 2300 cycles of softmax (1024 of them exponentials) and 1500 for
-// 16 products of 64 cycles and their latencies, of which the other tile hides half.  Tried and
-// not kept: a quarter of the exponentials as polynomials on the fma units (slower or even),
-// two threads per query (6% slower: the exchange of maxima), turns to and fro.
+// sequences up to 6007, 64/8 heads: 1245, 1126, 1074, 1040, 1005 us, and 934 with eight heads to a
+// tile (1067 TFLOP/s).  What bounds it: the chain of one tile, about 2300 cycles of softmax (1024
+// of them exponentials) and 1500 for 16 products of 64 cycles and their latencies, of which the
+// other tile hides half.  Tried and not kept: a quarter of the exponentials as polynomials on
+// the fma units (slower or even), two threads per query (6% slower: the exchange of maxima),
+// turns to and fro.
+//
+// Query heads of a k/v head may share tiles, whose rows then are the heads of one query, then those
+// of the next (packed_heads).
 //
 // Few queries over many keys leave SMs idle: then a cluster of 2, 4 or 8 blocks shares a pair
 // of tiles, each block taking a run of the key tiles; their (m, l, o) stay in shared memory,
 // and every block joins its share of the rows from all of them.  37 queries after 2011 keys,
-// 16 heads of 64: 39 us on one block per head, 16 on four (14 with what came after); one
-// query after 8000 keys, 8 heads of 128: 148 us on one, 26 (23) on eight.
+// 16/4 heads of 64: 39 us on one block per head, 16 on four, 12 with four heads to a tile; one
+// query after 8000 keys, 8 heads of 128: 148 us on one, 23 on eight.
 //
 // Rows that no query may see: scores of keys past a row's limit are replaced before they are
 // used; values past the sequence's end are zeroed in shared memory.  Inside a sequence a
@@ -65,7 +69,7 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr int MOST = 64;                  // keys whose weights are handed over first
 constexpr float KEEP = 8.f;               // log2 of the largest weight under a kept maximum
 
-// A pair of tiles of one head: its sequence's first rows and lengths (pair -1: no more).
+// A pair of tiles of one pack of heads: its sequence's first rows and lengths (pair -1: no more).
 struct Work {
   int pair, h, q0, k0, lq, lk;
 };
@@ -245,7 +249,7 @@ __device__ __forceinline__ Work find_work(const AttentionArgs& A, int slot, int 
       if (q0 < 0 || q1 < q0 || q1 > A.total_q || k0 < 0 || k1 < k0 || k1 > A.total_k)
         set_error(st, GPTQ_ERR_INVALID_ARG, b, STAGE_ATTENTION);
       else
-        pairs = (int)(((int64_t)(q1 - q0) + 2 * TQ - 1) / (2 * TQ));
+        pairs = (int)((((int64_t)(q1 - q0) << A.packed) + 2 * TQ - 1) / (2 * TQ));
     }
     int incl = pairs;
 #pragma unroll
@@ -271,12 +275,23 @@ __device__ __forceinline__ Work find_work(const AttentionArgs& A, int slot, int 
 __device__ __forceinline__ Tile make_tile(const AttentionArgs& A, int first, int lq, int lk) {
   Tile t;
   t.row0 = first;
-  t.rows = max(0, min(TQ, lq - first));
+  t.rows = max(0, min(TQ, (lq << A.packed) - first));
   t.shift = A.causal ? 1 + lk - lq : lk;
-  const int last = t.rows > 0 ? (A.causal ? min(lk, first + t.rows - 1 + t.shift) : lk) : 0;
+  const int last = t.rows > 0 ? (A.causal ? min(lk, ((first + t.rows - 1) >> A.packed) + t.shift) : lk) : 0;
   t.blocks = last > 0 ? (last + TQ - 1) / TQ : 0;
   return t;
 }
+
+// Row `row` of a pair: its query, head, and how many keys it sees (0 behind the sequence's end).
+struct Row {
+  int query, head, seen;
+  __device__ __forceinline__ Row(const AttentionArgs& A, const Work& w, int row) {
+    const int i = w.pair * 2 * TQ + row;
+    query = i >> A.packed;
+    head = (w.h << A.packed) + (i & ((1 << A.packed) - 1));
+    seen = query < w.lq ? max(0, min(w.lk, A.causal ? query + 1 + w.lk - w.lq : w.lk)) : 0;
+  }
+};
 
 // The two tiles of a pair, as one block of `size` that share it takes them.
 struct Tiles {
@@ -298,12 +313,6 @@ struct Tiles {
     tail = blocks > 0 && first + blocks * TQ > w.lk ? w.lk - first - (blocks - 1) * TQ : 0;
   }
 };
-
-// Keys that query `row` of a pair sees (0 behind the sequence's end).
-__device__ __forceinline__ int seen_of(const AttentionArgs& A, const Work& w, int row) {
-  const int i = w.pair * 2 * TQ + row;
-  return i < w.lq ? max(0, min(w.lk, A.causal ? i + 1 + w.lk - w.lq : w.lk)) : 0;
-}
 
 // One query against the keys it sees, one after another, by a whole warp (see above).
 template <typename T>
@@ -383,12 +392,11 @@ __device__ __forceinline__ void join_parts(const AttentionArgs& A, AttnSmem<KD>&
     asm volatile("ld.shared::cluster.b32 %0, [%1];"
                  : "=r"(ok) : "r"(tc::map_to_cta(tc::smem_u32(&S.valid), lane)) : "memory");
   if (!__all_sync(0xffffffffu, ok)) return;
-  const int q0 = S.mine.q0, k0 = S.mine.k0, lq = S.mine.lq, lk = S.mine.lk, h = S.mine.h;
-  const int hk = h / (A.heads_q / A.heads_kv);
-  const int rows = min(2 * TQ, lq - S.mine.pair * 2 * TQ);
+  const Work w = S.mine;
+  const int hk = (w.h << A.packed) / (A.heads_q / A.heads_kv);
+  const int rows = min(2 * TQ, (w.lq << A.packed) - w.pair * 2 * TQ);
   for (int r = (int)rank + warp * (int)size; r < rows; r += (int)size * (ATHREADS / 32)) {
-    const int i = S.mine.pair * 2 * TQ + r;               // the query in its sequence
-    const int limit = max(0, min(lk, A.causal ? i + 1 + lk - lq : lk));
+    const Row me(A, w, r);
     const uint32_t ml_at = tc::smem_u32(S.q[0]) + r * 8;
     // feature piece: V consecutive values per lane
     const uint32_t o_at = tc::smem_u32(S.kv[0]) + (part_at<KD>(r, lane * V / 4) + lane * V % 4) * 4;
@@ -415,30 +423,30 @@ __device__ __forceinline__ void join_parts(const AttentionArgs& A, AttnSmem<KD>&
     for (int e = 0; e < V; ++e) acc[e] = 0.f;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      const float w = __shfl_sync(0xffffffffu, f, c);
+      const float x = __shfl_sync(0xffffffffu, f, c);
       if (live >> c & 1) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = fmaf(o[c][e], w, acc[e]);
+        for (int e = 0; e < V; ++e) acc[e] = fmaf(o[c][e], x, acc[e]);
       }
     }
     const float inv = 1.f / l;
     bool nan = false;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      acc[e] = limit == 0 ? 0.f : acc[e] * inv;
+      acc[e] = me.seen == 0 ? 0.f : acc[e] * inv;
       nan |= acc[e] != acc[e];
     }
-    T* dst = static_cast<T*>(A.o) + (int64_t)(q0 + i) * A.o_ts + h * A.o_hs;
+    T* dst = static_cast<T*>(A.o) + (int64_t)(w.q0 + me.query) * A.o_ts + me.head * A.o_hs;
     if (lane * V < A.head_dim) {
-      uint32_t w[V / 2];
+      uint32_t u[V / 2];
 #pragma unroll
-      for (int e = 0; e < V / 2; ++e) w[e] = pack2(acc[2 * e], acc[2 * e + 1], T());
-      if constexpr (V == 4) *reinterpret_cast<uint2*>(dst + lane * V) = make_uint2(w[0], w[1]);
-      else *reinterpret_cast<uint32_t*>(dst + lane * V) = w[0];
+      for (int e = 0; e < V / 2; ++e) u[e] = pack2(acc[2 * e], acc[2 * e + 1], T());
+      if constexpr (V == 4) *reinterpret_cast<uint2*>(dst + lane * V) = make_uint2(u[0], u[1]);
+      else *reinterpret_cast<uint32_t*>(dst + lane * V) = u[0];
     }
     if (__any_sync(0xffffffffu, nan)) {
       __syncwarp();                                       // the row's first values before its second
-      seen_row<T>(A, q0 + i, h, hk, k0, limit);
+      seen_row<T>(A, w.q0 + me.query, me.head, hk, w.k0, me.seen);
     }
   }
 }
@@ -458,12 +466,13 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int size = SPLIT ? (int)cluster_size() : 1, rank = SPLIT ? (int)tc::cluster_rank() : 0;
   const int step = (int)gridDim.x / size;                 // pairs of tiles taken at once
+  const int packs = A.heads_q >> A.packed;
   int at = (int)blockIdx.x / size;                        // the loader's pair (of every head), then at + step, ...
   Work w{-1, 0, 0, 0, 0, 0};
 
   if (warp == 9) tc::tmem_alloc<512>(&S.tmem_base);
   int b0 = 0, base = 0;
-  if (warp == 8) w = find_work(A, at / A.heads_q, at % A.heads_q, b0, base, st);
+  if (warp == 8) w = find_work(A, at / packs, at % packs, b0, base, st);
   if (warp == 0 && lane == 0) {
     S.skip = has_error(st);
     S.abort = 0;
@@ -516,7 +525,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
         }
         if (w.pair < 0) break;
         const Tiles tl(A, w, size, rank);
-        const int hk = w.h / (A.heads_q / A.heads_kv);
+        const int hk = (w.h << A.packed) / (A.heads_q / A.heads_kv);
         int ok = 1;
         if (lane == 0) {
           for (int i = 0; i < 2 * tl.blocks && ok; ++i, ++it) {
@@ -526,7 +535,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
               tc::mbar_arrive_expect_tx(&S.q_full[i], TILE);
 #pragma unroll
               for (int c = 0; c < KD / 64; ++c)
-                tma_load_3d(S.q[i] + c * (TQ * 128), &tq, &S.q_full[i], c * 64, w.h, w.q0 + tl.t[i].row0);
+                tma_load_3d(S.q[i] + c * (TQ * 128), &tq, &S.q_full[i], c * 64, w.h << A.packed,
+                            w.q0 + (tl.t[i].row0 >> A.packed));
               S.q_armed[i] = ++q_uses[i];
             }
             const int s = it % NST;
@@ -544,7 +554,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
         at += step;
         w.pair = -1;
         if (!SPLIT && at < pairs)
-          w = find_work(A, at / A.heads_q, at % A.heads_q, b0, base, st);
+          w = find_work(A, at / packs, at % packs, b0, base, st);
       }
     } else if (warp == 9) {
       // The whole warp walks the loop, so that the products' descriptors stay in uniform
@@ -646,7 +656,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
         {
           const Tiles tl(A, w, size, rank);
           blocks = tl.t[t].blocks;
-          see0 = seen_of(A, w, t * TQ + r) - tl.first;
+          see0 = Row(A, w, t * TQ + r).seen - tl.first;
         }
         const float c0 = A.scale * LOG2E;
         const float c = c0 > 0.f ? c0 : 1.f;
@@ -756,8 +766,10 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
           if (ok) {
             tc::tc_fence_after();
             const Work v = handed(n);
-            const int i0 = v.pair * 2 * TQ + t * TQ + r, limit = seen_of(A, v, t * TQ + r);
-            T* dst = static_cast<T*>(A.o) + (int64_t)(v.q0 + i0) * A.o_ts + v.h * A.o_hs;
+            const Row me(A, v, t * TQ + r);
+            const int limit = me.seen;
+            const bool mine = me.query < v.lq;
+            T* dst = static_cast<T*>(A.o) + (int64_t)(v.q0 + me.query) * A.o_ts + me.head * A.o_hs;
             const float inv = limit > 0 ? 1.f / l : 0.f;
             bool nan = false;
 #pragma unroll 1
@@ -769,16 +781,18 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 o[e] = limit > 0 ? o[e] * inv : 0.f;
                 nan |= o[e] != o[e];
               }
-              if (i0 < v.lq) {
+              if (mine) {
                 if (i < A.head_dim) store8(dst + i, o);
                 if (i + 8 < A.head_dim) store8(dst + i + 8, o + 8);
               }
             }
-            unsigned again = __ballot_sync(0xffffffffu, nan && i0 < v.lq);
+            unsigned again = __ballot_sync(0xffffffffu, nan && mine);
+            __syncwarp();                                 // a row's first values before its second
             while (again != 0) {
               const int src = __ffs(again) - 1;
               again &= again - 1;
-              seen_row<T>(A, v.q0 + i0 - lane + src, v.h, v.h / (A.heads_q / A.heads_kv), v.k0, __shfl_sync(0xffffffffu, limit, src));
+              const Row row(A, v, t * TQ + r - lane + src);
+              seen_row<T>(A, v.q0 + row.query, row.head, row.head / (A.heads_q / A.heads_kv), v.k0, row.seen);
             }
           }
         }
@@ -814,11 +828,30 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
   }
 }
 
+// Pairs of tiles, of every pack of heads, at most.
+int64_t most_pairs(const AttentionArgs& A) {
+  return ((((int64_t)A.total_q << A.packed) / (2 * TQ)) + A.count) * (A.heads_q >> A.packed);
+}
+
+// Query heads of one k/v head share tiles (2^packed of them, their rows the queries' heads in
+// turn): until an average sequence fills a tile, and on while there is work for every SM four
+// times over (a pair of tiles then spans fewer queries, whose causal limits are closer: packed
+// sequences, 64/8 heads: 1005 us with none, 934 with eight; 64 queries, 32/8 heads: 8 us with
+// none or two, 11 with four, whose blocks are too few).
+int packed_heads(AttentionArgs A) {
+  const int per = A.heads_q / A.heads_kv;
+  A.packed = 0;
+  while (A.packed < 4 && per % (2 << A.packed) == 0 && ((int64_t)A.total_q << (A.packed + 1)) <= INT32_MAX - 2 * TQ &&
+         ((((int64_t)A.total_q / A.count) << A.packed) < TQ || most_pairs(A) >= 4 * SMS))
+    ++A.packed;
+  return A.packed;
+}
+
 // Blocks that share a pair of tiles: as many as run at once (74 clusters of two, 33 of four,
 // 15 of eight at this shared memory: a cluster stays in one part of the chip) and have two
 // key tiles or more of an average sequence.
 int cluster_of(const AttentionArgs& A) {
-  const int64_t work = (A.total_q / (2 * TQ) + (int64_t)A.count) * A.heads_q, tiles = A.total_k / A.count / TQ;
+  const int64_t work = most_pairs(A), tiles = A.total_k / A.count / TQ;
   if (work <= 15 && tiles >= 16) return 8;
   if (work <= 33 && tiles >= 8) return 4;
   return work <= 74 && tiles >= 4 ? 2 : 1;
@@ -830,8 +863,7 @@ int launch(const AttentionArgs& A, const CUtensorMap& tq, const CUtensorMap& tk,
   const size_t smem = sizeof(AttnSmem<KD>) + 1024;
   auto* kernel = attention_kernel<KD, T, SPLIT>;
   GPTQ_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  // at most total_q / 256 + count pairs of tiles, of every head, and one block that reads every bound
-  const int64_t pairs = (A.total_q / (2 * TQ) + (int64_t)A.count) * A.heads_q + 1;
+  const int64_t pairs = most_pairs(A) + 1;                // and one block that reads every bound
   if (pairs * size > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(SPLIT ? pairs * size : (pairs < SMS ? pairs : SMS)));
@@ -856,25 +888,27 @@ int launch_any(const AttentionArgs& A, const CUtensorMap& tq, const CUtensorMap&
   return size > 1 ? launch<KD, T, true>(A, tq, tk, tv, size, st, s) : launch<KD, T, false>(A, tq, tk, tv, 1, st, s);
 }
 
-// [tokens, heads, head_dim] in boxes of 128 tokens by 64 features; features past head_dim
-// and tokens past the end read as 0.
+// [tokens, heads, head_dim] in boxes of 128 rows (tokens, each of 2^packed heads) by 64
+// features; features past head_dim and tokens past the end read as 0.
 int head_map(CUtensorMap* map, CUtensorMapDataType dt, const void* p, int tokens, int heads, int head_dim, int64_t ts,
-             int64_t hs) {
+             int64_t hs, int packed) {
   return make_tmap_3d(map, dt, p, (uint64_t)head_dim, (uint64_t)heads, (uint64_t)tokens, (uint64_t)hs * 2,
-                      (uint64_t)ts * 2, 64, 1, TQ, CU_TENSOR_MAP_SWIZZLE_128B);
+                      (uint64_t)ts * 2, 64, 1u << packed, (uint32_t)(TQ >> packed), CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace
 
-int launch_attention(const AttentionArgs& A, int dtype, int32_t* st, cudaStream_t s) {
+int launch_attention(const AttentionArgs& args, int dtype, int32_t* st, cudaStream_t s) {
+  AttentionArgs A = args;
+  A.packed = packed_heads(A);
   CUtensorMap tq, tk, tv;
   const CUtensorMapDataType dt = dtype == GPTQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  int rc = head_map(&tq, dt, A.q, A.total_q, A.heads_q, A.head_dim, A.q_ts, A.q_hs);
+  int rc = head_map(&tq, dt, A.q, A.total_q, A.heads_q, A.head_dim, A.q_ts, A.q_hs, A.packed);
   if (rc != GPTQ_OK) return rc;
   tk = tv = tq;                           // without any key nothing is loaded through them
   if (A.total_k > 0) {
-    rc = head_map(&tk, dt, A.k, A.total_k, A.heads_kv, A.head_dim, A.k_ts, A.k_hs);
-    if (rc == GPTQ_OK) rc = head_map(&tv, dt, A.v, A.total_k, A.heads_kv, A.head_dim, A.v_ts, A.v_hs);
+    rc = head_map(&tk, dt, A.k, A.total_k, A.heads_kv, A.head_dim, A.k_ts, A.k_hs, 0);
+    if (rc == GPTQ_OK) rc = head_map(&tv, dt, A.v, A.total_k, A.heads_kv, A.head_dim, A.v_ts, A.v_hs, 0);
     if (rc != GPTQ_OK) return rc;
   }
   TraceScope ts("attention", "", 0.0, s);

@@ -143,6 +143,7 @@ struct AttentionArgs {
   int count, total_q, total_k, heads_q, heads_kv, head_dim;
   float scale;
   int causal;
+  int packed;                             // log2 of the query heads that share a tile (set by the launch)
 };
 int launch_attention(const AttentionArgs& A, int dtype, int32_t* st, cudaStream_t s);
 // The 4-bit cache: [0] keys, [1] values (layout in kv4.cuh).

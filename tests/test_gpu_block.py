@@ -363,6 +363,33 @@ def test_attention_few_queries_masked_rows_take_no_part(dt, d):
     assert torch.isnan(got[20:40, :2]).all() and torch.isnan(got[25:40, 2:]).all()
 
 
+# heads that share tiles: 2 of 6, 16 of 32, 16 of 16, 4 of 4, 8 of 8 per k/v head
+PACKED_CASES = [
+    ([2, 61], [1500, 3], 12, 2, 64, HF, True),
+    ([3, 9, 0, 1], [200, 0, 4, 7], 32, 1, 128, BF, True),
+    ([17], [130], 16, 1, 72, BF, True),
+    ([40, 33], [-39, 100], 8, 2, 128, HF, True),
+    ([1] * 9, [255, 0, 1, 128, 127, 126, 300, 64, 5], 16, 2, 128, BF, True),
+    ([100, 30], [0, 0], 4, 1, 64, BF, False),
+]
+
+
+@pytest.mark.parametrize("lens,past,hq,hk,d,dt,causal", PACKED_CASES)
+def test_attention_heads_that_share_tiles(lens, past, hq, hk, d, dt, causal):
+    test_attention(lens, past, hq, hk, d, dt, causal)
+
+
+def test_attention_heads_that_share_tiles_masked_rows():
+    q, k, v, cq, ck = _attn_inputs([20, 9], [30, 0], 8, 1, 128, BF)
+    v2 = v.clone()
+    v2[35] = float("nan")                                    # queries 0 .. 4 of sequence 0 do not see it
+    got = G.attention(q, k, v2, _int(cq), _int(ck))
+    ref, tol = _attn_tol(_np(q), _np(k), _np(v), cq, ck, 128 ** -0.5, True, BF, U[BF])
+    rows = list(range(5)) + list(range(20, 29))
+    _close(got[rows], ref[rows], tol[rows], "rows that see none")
+    assert torch.isnan(got[5:20]).all()
+
+
 @pytest.mark.parametrize("hq,hk,d,dt,causal", [(8, 2, 128, BF, True), (6, 6, 64, HF, True), (9, 3, 80, BF, False)])
 def test_attention_many_pairs_per_block(hq, hk, d, dt, causal):
     """Far more pairs of tiles than SMs, of every size, empty sequences among them: blocks go from pair to pair."""
