@@ -10,13 +10,16 @@
 // Sums are fp32; the layer norm takes its squares from the centred values (a second
 // pass over registers, not over memory), so a large mean costs no digits.
 //
-// Bound: HBM.  A row is read once into registers (8 values per thread up to d = 256, 16 up to
-// 4096, 32 above: fewer threads meet at the barriers, 4000 rows of 8192 with norms on both
-// sides 84 us with 16, 65 with 32) and every statistic is taken there; x, y and the gate are
-// read and xn and h written once; the parameters come from L1 and are applied a row piece at a
-// time, so that x and y are all that a thread holds.  Rows of up to 512 values take a warp each,
-// of up to 128 and 64 a half and a quarter of one (no block barrier; 200,000 rows of 64: 99 us
-// with a warp each, 32 so), longer rows a block.  Where rows do not start on 16-byte boundaries (an
+// Bound: HBM.  A row is read once into registers and every statistic is taken there; x, y and
+// the gate are read and xn and h written once; the parameters come from L1 and are applied a
+// row piece at a time, so that x and y are all that a thread holds (of 24 values or more y
+// alone: x is read when it is added).  Rows of up to 1024 values take a warp each, 8 to 32
+// values per thread, rows of up to 128 and 64 a half and a quarter of one (no block barrier;
+// 200,000 rows of 64: 99 us with a warp each, 32 so; 40,906 rows of 576: 73 us with a block
+// each, 50 so), longer rows a block of 32 values per thread (fewer threads meet at the
+// barriers: 4000 rows of 8192 with norms on both sides 84 us with 16 values, 65 so; one row of
+// 4096 though takes 8 us with 16 and 10 with 32, hence 16 where rows are few).  Where rows do
+// not start on 16-byte boundaries (an
 // odd d or stride) a thread of a 16-bit stream still takes eight consecutive values: it reads
 // the aligned 16-byte pieces that hold them and shifts, and writes by way of shared memory,
 // where each thread picks up what belongs to one aligned piece; single values only at a row's
@@ -50,7 +53,7 @@ struct NormArgs {
 };
 
 constexpr int ANY = -1;
-constexpr int LONG = 4096;                // values of a row above which a thread takes 32
+constexpr int FEW = 148 * 2;              // rows below which their latency counts, not their number
 
 // A row's threads and their places.  T = 0: any number of threads with eight consecutive
 // values per piece, which lie on 16-byte boundaries; ANY: the same on any boundaries; else T
@@ -305,16 +308,20 @@ void launch(const NormArgs& A, bool vec, const int32_t* st, cudaStream_t s) {
   const dim3 warps(lanes, 256 / lanes);
   const unsigned groups = (unsigned)cdiv(A.tokens, 256 / lanes);
   if (vec) {
-    const unsigned thr = (unsigned)(cdiv(cdiv(A.d, A.d <= LONG ? 16 : 32), 32) * 32);
+    const bool few = A.tokens < FEW && A.d <= 16384;
+    const unsigned thr = (unsigned)(cdiv(cdiv(A.d, few ? 16 : 32), 32) * 32);
     if (A.d <= 256) add_norm_kernel<TX, 1, 0, true, 256><<<groups, warps, 0, s>>>(A, st);
     else if (A.d <= 512) add_norm_kernel<TX, 2, 0, true, 256><<<groups, warps, 0, s>>>(A, st);
-    else if (A.d <= LONG) add_norm_kernel<TX, 2, 0, false, 1024><<<rows, thr, 0, s>>>(A, st);
+    else if (few) add_norm_kernel<TX, 2, 0, false, 1024><<<rows, thr, 0, s>>>(A, st);
+    else if (A.d <= 768) add_norm_kernel<TX, 3, 0, true, 256><<<groups, warps, 0, s>>>(A, st);
+    else if (A.d <= 1024) add_norm_kernel<TX, 4, 0, true, 256><<<groups, warps, 0, s>>>(A, st);
     else add_norm_kernel<TX, 4, 0, false, 1024><<<rows, thr, 0, s>>>(A, st);
     return;
   }
   if constexpr (sizeof(TX) == 2) {
     if (A.d <= 256) add_norm_kernel<TX, 1, ANY, true, 256><<<groups, warps, 256 * 16, s>>>(A, st);
     else if (A.d <= 512) add_norm_kernel<TX, 2, ANY, true, 256><<<groups, warps, 512 * 16, s>>>(A, st);
+    else if (A.d <= 768) add_norm_kernel<TX, 3, ANY, true, 256><<<groups, warps, 768 * 16, s>>>(A, st);
     else if (A.d <= 16384) {
       const unsigned thr = (unsigned)(cdiv(cdiv(A.d, 16), 32) * 32);
       const size_t smem = (size_t)thr * 2 * 16;
