@@ -120,6 +120,15 @@ def test_add_norm(tokens, d, xt, yt, pt, post, gate, center, bias, alpha):
     assert xi is X and torch.equal(X, xn) and torch.equal(h3, h)
 
 
+@pytest.mark.parametrize("d,xt,yt,post,gate,center", [
+    (64, BF, FF, False, "token", False), (96, HF, HF, True, "feature", True), (520, HF, BF, False, "token", False),
+    (776, BF, BF, True, "feature", True), (1024, FF, HF, True, None, False), (1536, BF, FF, True, "token", True),
+    (4096, HF, FF, False, None, False), (12008, BF, HF, True, "feature", True), (20000, FF, FF, False, "token", False),
+    (700, FF, BF, True, "feature", True), (701, HF, FF, True, "token", True)])
+def test_add_norm_many_rows(d, xt, yt, post, gate, center):
+    test_add_norm(310, d, xt, yt, xt, post, gate, center, post, 0.5)
+
+
 def test_add_norm_strided_rows_and_neighbours():
     rng = np.random.default_rng(5)
     for pad in (8, 3):                    # rows on 16-byte boundaries, and not
