@@ -32,9 +32,11 @@
  * - Argument errors are returned synchronously (nothing is enqueued).
  *   Errors found on the device (a non-positive Cholesky pivot, non-finite
  *   values, a bounded wait that gave up) are recorded in a caller-provided
- *   device status block `d_status` (int32[4]: code, info, stage, reserved):
- *   the first error wins, and every later kernel that sees a non-zero code
- *   skips its work.  Clear it with gptq_status_reset() before a layer and read
+ *   device status block `d_status` (int32[4]: code, info, stage, and the number
+ *   of the call that recorded it where that call goes on): the first error
+ *   wins, and every later kernel that sees a non-zero code skips its work.  A
+ *   call whose text says what becomes of a bad token does just that, and the
+ *   rest of its work whatever it records itself.  Clear it with gptq_status_reset() before a layer and read
  *   it with gptq_status_read(), which synchronizes the stream.
  * - Matrices are row-major with the stated leading dimensions.
  * - The library targets sm_100a (B200) only.

@@ -11,7 +11,7 @@
 namespace gptq {
 
 // Index of the fields of the caller's device status block.
-enum { ST_CODE = 0, ST_INFO = 1, ST_STAGE = 2 };
+enum { ST_CODE = 0, ST_INFO = 1, ST_STAGE = 2, ST_LAUNCH = 3 };
 
 // Stage ids recorded in d_status[ST_STAGE] next to an error.
 enum {
@@ -35,6 +35,28 @@ __device__ __forceinline__ bool has_error(const int32_t* st) {
   return *reinterpret_cast<const volatile int32_t*>(st + ST_CODE) != 0;
 }
 
+// For launches that go on past the errors they record (a bad token is left out, the others are
+// not): has_error would stop the blocks, or the warps, that look after another one recorded
+// something.  `launch` is the call's number (next_launch()), kept beside the error.
+__device__ __forceinline__ void set_own_error(int32_t* st, int launch, int code, int info, int stage) {
+  if (st == nullptr || has_error(st)) return;
+  *reinterpret_cast<volatile int32_t*>(st + ST_LAUNCH) = launch;     // (the same value from every block)
+  __threadfence();
+  set_error(st, code, info, stage);
+}
+
+// An error that was there before the launch.  Where threads of a block depend on one another
+// one thread asks for all.  From here on the error is nobody's own: a graph that holds the call
+// which recorded it stops there too when it is replayed.
+__device__ __forceinline__ bool stopped(int32_t* st, int launch) {
+  if (!has_error(st)) return false;
+  __threadfence();
+  volatile int32_t* by = st + ST_LAUNCH;
+  if (*by == launch) return false;
+  *by = 0;
+  return true;
+}
+
 template <typename T> __device__ __forceinline__ float load_as_float(const T* p);
 template <> __device__ __forceinline__ float load_as_float<float>(const float* p) { return *p; }
 template <> __device__ __forceinline__ float load_as_float<__half>(const __half* p) { return __half2float(*p); }
@@ -50,6 +72,7 @@ __host__ __device__ constexpr size_t align_up(size_t v, size_t a) { return (v + 
 namespace gptq {
 // Host-side count of enqueued kernels (see gptq_kernel_launches).
 void count_launch();
+int next_launch();                    // a call's number for set_own_error: never 0, another for every call
 void count_launches(int64_t delta);   // a replayed graph's kernels (or, negative, a captured graph's)
 }  // namespace gptq
 

@@ -14,6 +14,14 @@ namespace gptq {
 namespace {
 std::atomic<uint64_t> g_launches{0};
 }
+int next_launch() {
+  static std::atomic<uint32_t> n{0};
+  uint32_t v;
+  do {
+    v = n.fetch_add(1, std::memory_order_relaxed) + 1;
+  } while (v == 0);
+  return (int)v;
+}
 void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 void count_launches(int64_t delta) { g_launches.fetch_add((uint64_t)delta, std::memory_order_relaxed); }
 }  // namespace gptq

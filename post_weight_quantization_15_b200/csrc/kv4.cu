@@ -42,21 +42,27 @@ constexpr int THREADS = 256;
 constexpr int MOST = 64;                  // tokens of a block
 constexpr int ENOUGH = 148 * 8;           // blocks that fill the SMs
 
-// Tokens t0 .. t0 + n - 1 of the batch: the first head's row in the cache of each, or -1.
-__device__ __forceinline__ void find_rows(const KV4Cache& C, const int32_t* table, int width, const int32_t* cu,
-                                          const int32_t* start, int count, int t0, int n, int64_t* rows, int32_t* st) {
+// Tokens t0 .. t0 + n - 1 of the batch: the first head's row in the cache of each, or -1.  False,
+// for the whole block, after an earlier launch's error; those of this launch (other blocks' tokens)
+// stop nobody.
+__device__ __forceinline__ bool find_rows(const KV4Cache& C, const int32_t* table, int width, const int32_t* cu,
+                                          const int32_t* start, int count, int t0, int n, int64_t* rows, int32_t* st,
+                                          int launch) {
+  __shared__ int skip;
+  if (threadIdx.x == THREADS - 1) skip = stopped(st, launch);
   if ((int)threadIdx.x < n) {
     const int t = t0 + (int)threadIdx.x, b = packed_sequence(cu, count, t);
     int64_t row = -1;
     if (b >= 0) {
       const int64_t pos = (start != nullptr ? (int64_t)start[b] : 0) + (t - cu[b]);
       const int page = kv4_page(C, table, width, b, pos);
-      if (page < 0) set_error(st, GPTQ_ERR_INVALID_ARG, t, STAGE_KV4);
+      if (page < 0) set_own_error(st, launch, GPTQ_ERR_INVALID_ARG, t, STAGE_KV4);
       else row = kv4_row(C, page, 0, (int)(pos & (C.page_size - 1)));
     }
     rows[threadIdx.x] = row;
   }
   __syncthreads();
+  return !skip;
 }
 
 // A thread's place among a token's `per` units: unit u0 of every subs-th token, or units u0,
@@ -164,11 +170,10 @@ template <typename T, int N>
 __global__ void __launch_bounds__(THREADS) kv4_append_kernel(const __grid_constant__ KV4Cache C,
                                                              const __grid_constant__ KVInput in, const int32_t* table,
                                                              int width, const int32_t* cu, const int32_t* start,
-                                                             int count, int tokens, int per_block, int32_t* st) {
+                                                             int count, int tokens, int per_block, int32_t* st, int launch) {
   __shared__ int64_t rows[MOST];
-  if (has_error(st)) return;
   const int t0 = (int)blockIdx.x * per_block, n = min(per_block, tokens - t0);
-  find_rows(C, table, width, cu, start, count, t0, n, rows, st);
+  if (!find_rows(C, table, width, cu, start, count, t0, n, rows, st, launch)) return;
   const Units U(C.heads * (C.head_dim / (8 * N)));
   const int words = C.head_dim / 8, lanes = C.group / (8 * N), groups = C.head_dim / C.group;
   const int lw = __ffs(words / N) - 1, ll = __ffs(lanes) - 1;
@@ -203,7 +208,7 @@ __global__ void __launch_bounds__(THREADS) kv4_append_kernel(const __grid_consta
 #pragma unroll
           for (int c = 0; c < N; ++c) word[c] = 0;
           par = __halves2half2(__ushort_as_half((unsigned short)0x7fffu), __ushort_as_half((unsigned short)0));
-          if (lane == 0) set_error(st, GPTQ_ERR_NONFINITE, t0 + i, STAGE_KV4);
+          if (lane == 0) set_own_error(st, launch, GPTQ_ERR_NONFINITE, t0 + i, STAGE_KV4);
         }
         const int64_t at = row + (int64_t)head * C.page_size;
 #pragma unroll
@@ -218,11 +223,10 @@ template <typename T>
 __global__ void __launch_bounds__(THREADS) kv4_read_kernel(const __grid_constant__ KV4Cache C, const int32_t* table,
                                                            int width, const int32_t* cu, const int32_t* start,
                                                            int count, int tokens, int per_block, T* k, T* v,
-                                                           int32_t* st) {
+                                                           int32_t* st, int launch) {
   __shared__ int64_t rows[MOST];
-  if (has_error(st)) return;
   const int t0 = (int)blockIdx.x * per_block, n = min(per_block, tokens - t0);
-  find_rows(C, table, width, cu, start, count, t0, n, rows, st);
+  if (!find_rows(C, table, width, cu, start, count, t0, n, rows, st, launch)) return;
   const Units U(C.heads * (C.head_dim / 16));
   if (U.sub >= U.subs) return;
   const int words = C.head_dim / 8, lanes = C.group / 16, groups = C.head_dim / C.group;
@@ -281,7 +285,8 @@ int launch_kv4_append(const KV4Cache& C, const void* k, int64_t k_ts, int64_t k_
   const int n = tokens_per_block(C, tokens, features);
   const unsigned grd = (unsigned)cdiv(tokens, n);
   TraceScope ts("kv4_append", "byte", tokens * (token_bytes(C) + 4.0 * C.heads * C.head_dim), s);
-  auto go = [&](auto* kernel) { kernel<<<grd, THREADS, 0, s>>>(C, in, table, width, cu, start, count, tokens, n, st); };
+  const int launch = next_launch();
+  auto go = [&](auto* kernel) { kernel<<<grd, THREADS, 0, s>>>(C, in, table, width, cu, start, count, tokens, n, st, launch); };
   if (dtype == GPTQ_F16) go(features == 32 ? kv4_append_kernel<__half, 4> : kv4_append_kernel<__half, 2>);
   else go(features == 32 ? kv4_append_kernel<__nv_bfloat16, 4> : kv4_append_kernel<__nv_bfloat16, 2>);
   GPTQ_LAUNCH_CHECK();
@@ -293,9 +298,11 @@ int launch_kv4_read(const KV4Cache& C, const int32_t* table, int width, const in
   const int n = tokens_per_block(C, tokens, 16);
   const unsigned grd = (unsigned)cdiv(tokens, n);
   TraceScope ts("kv4_read", "byte", tokens * (token_bytes(C) + (dtype == GPTQ_F32 ? 8.0 : 4.0) * C.heads * C.head_dim), s);
+  const int launch = next_launch();
   auto go = [&](auto* p) {
     using T = std::remove_pointer_t<decltype(p)>;
-    kv4_read_kernel<T><<<grd, THREADS, 0, s>>>(C, table, width, cu, start, count, tokens, n, p, static_cast<T*>(v), st);
+    kv4_read_kernel<T><<<grd, THREADS, 0, s>>>(C, table, width, cu, start, count, tokens, n, p, static_cast<T*>(v), st,
+                                               launch);
   };
   if (dtype == GPTQ_F32) go(static_cast<float*>(k));
   else if (dtype == GPTQ_F16) go(static_cast<__half*>(k));
