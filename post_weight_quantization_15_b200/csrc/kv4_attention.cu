@@ -76,6 +76,7 @@ struct KvaArgs {
   int width, count, per, sets, rows;      // per: query heads of a k/v head, in sets of up to 8 (rows)
   float scale;
   int half;                               // q and o are fp16 (else bf16)
+  int launch;                             // the call's number, for the errors it records
 };
 
 // Sequence b's tiles (one head set); 0 for a length that the table does not hold.
@@ -286,7 +287,7 @@ kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
   Smem& S = *reinterpret_cast<Smem*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, j = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;");
-  if (threadIdx.x == 0) S.skip = has_error(st);
+  if (threadIdx.x == 0) S.skip = stopped(st, A.launch);
   const int heads = A.C.heads * A.sets;
   int64_t all = 0;
   for (int b = lane; b < A.count; b += 32) all += slots_of(tiles_of(A, b), heads);
@@ -325,7 +326,7 @@ kv4_attention_kernel(const __grid_constant__ KvaArgs A, int32_t* st) {
             if (pos < len) {
               page = kv4_page(A.C, A.table, A.width, p.b, pos);
               if (page < 0) {
-                set_error(st, GPTQ_ERR_INVALID_ARG, p.b, STAGE_KV4_ATTENTION);
+                set_own_error(st, A.launch, GPTQ_ERR_INVALID_ARG, p.b, STAGE_KV4_ATTENTION);
                 page = 0;
               } else {
                 ok |= 1 << k;
@@ -732,9 +733,13 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ K
   __shared__ float weight[MOST];
   __shared__ float ml[8][2];
   __shared__ long long sums[8][2];
+  __shared__ int skip;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hx = (int)blockIdx.x / A.rows, row = (int)blockIdx.x % A.rows, b = (int)blockIdx.y;
   const int heads = A.C.heads * A.sets;
+  // what the attention launch records is this call's own and stops no row: the answer is the same
+  // before and after it
+  if (threadIdx.x == 255) skip = stopped(st, A.launch);
   long long before = 0, all = 0;
   for (int i = (int)threadIdx.x; i < A.count; i += 256) {
     const int64_t n = slots_of(tiles_of(A, i), heads);
@@ -753,14 +758,13 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ K
   // every block waits for the attention launch: this launch's end stands for both
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int in_set = min(ROWS, A.per - (hx % A.sets) * ROWS);
-  if (row >= in_set) return;
+  if (skip || row >= in_set) return;
   const int q = hx / A.sets * A.per + (hx % A.sets) * ROWS + row;
   const int n = tiles_of(A, b), len = A.lengths[b];
   if (n == 0 && len != 0) {
-    if (threadIdx.x == 0) set_error(st, GPTQ_ERR_INVALID_ARG, b, STAGE_KV4_ATTENTION);
+    if (threadIdx.x == 0) set_own_error(st, A.launch, GPTQ_ERR_INVALID_ARG, b, STAGE_KV4_ATTENTION);
     return;
   }
-  if (has_error(st)) return;
   const int64_t at = (int64_t)b * A.o_ts + (int64_t)q * A.o_hs;
   if (n == 0) {
     const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -867,7 +871,7 @@ int launch_kv4_attention(const KV4Cache& C, const void* q, int64_t q_ts, int64_t
   const int per = heads_q / C.heads, rows = set_rows(per);
   KvaArgs A{C, q, o, q_ts, q_hs, o_ts, o_hs, table, lengths, static_cast<float*>(ws),
             static_cast<float*>(ws) + (size_t)2 * RUNS * rows * C.head_dim, width, count, per, head_sets(per), rows,
-            scale, dtype == GPTQ_F16};
+            scale, dtype == GPTQ_F16, next_launch()};
   TraceScope ts("kv4_attention", "", 0.0, s);
   if (C.head_dim == 64) return C.group == 32 ? launch<64, 32>(A, st, s) : launch<64, 64>(A, st, s);
   if (C.group == 32) return launch<128, 32>(A, st, s);

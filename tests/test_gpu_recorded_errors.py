@@ -150,3 +150,73 @@ def test_a_replayed_graph_stops_at_its_own_error():
     assert G.status_read(st)[0] == 0 and torch.equal(rk, good)
     for n, x in zip(TENSORS, want):
         assert _same_bits(getattr(cache, n), x), n
+
+
+# --------------------------------------------------------------------------- #
+# kv4_attention: 300 sequences, some of one warp's run, some of many, 8 heads
+# --------------------------------------------------------------------------- #
+def _attention_inputs(seed, hq=16, dt=BF):
+    rng = np.random.default_rng(seed)
+    lens = [int(n) for n in rng.integers(1, 90, 300)]
+    lens[100], lens[101], lens[200], lens[250] = 5000, 0, 3000, 0
+    table, pages = _pages(rng, lens, PAGE)
+    cache = G.kv4_alloc(pages, PAGE, HEADS, D, GROUP, device=_dev())
+    k, v = (_rand(rng, (sum(lens), HEADS, D), dt) for _ in range(2))
+    G.kv4_append(cache, k, v, table, _int(_cu(lens)), _int([0] * len(lens)))
+    q = _rand(rng, (len(lens), hq, D), dt)
+    return lens, cache, table, q, k, v
+
+
+# one bad sequence at a time: its cut of the work is that of a batch where it is empty
+@pytest.mark.parametrize("seq", [0, 100, 299])
+@pytest.mark.parametrize("length", [-1, 10 ** 6])
+def test_kv4_attention_beside_a_bad_length(seq, length):
+    lens, cache, table, q, _, _ = _attention_inputs(5)
+    without = list(lens)
+    without[seq] = 0
+    want = G.kv4_attention(q, cache, table, _int(without))
+    lens[seq] = length
+    for _ in range(3):
+        st, out = G.new_status(_dev()), torch.full_like(q, 7.0)
+        G.kv4_attention(q, cache, table, _int(lens), out=out, status=st)
+        assert G.status_read(st) == (INVALID, seq)
+        assert (out[seq] == 7).all()
+        out[seq] = want[seq]
+        assert torch.equal(out, want)
+    assert (want[[101, 250]] == 0).all()
+
+
+@pytest.mark.parametrize("seq", [0, 100, 299])
+@pytest.mark.parametrize("entry", [-1, 10 ** 6])
+def test_kv4_attention_beside_a_bad_page(seq, entry):
+    """The bad page's tokens take no part, in that sequence alone: the result is that of a sequence with the
+    other tokens."""
+    lens, cache, table, q, k, v = _attention_inputs(6)
+    want = G.kv4_attention(q, cache, table, _int(lens))
+    t2 = table.clone()
+    last = (lens[seq] - 1) // PAGE
+    t2[seq, last] = entry
+    for _ in range(3):
+        st, out = G.new_status(_dev()), torch.full_like(q, 7.0)
+        G.kv4_attention(q, cache, t2, _int(lens), out=out, status=st)
+        assert G.status_read(st) == (INVALID, seq)
+        got = out[seq].clone()
+        out[seq] = want[seq]
+        assert torch.equal(out, want)
+        # the sequence cut before that page, taken in other runs: each side's weights are off by 2^-11 of
+        # sum p|v| <= max|v| (a cached v may be half a step larger) and its result is rounded once (2^-8)
+        ref = G.kv4_attention(q[seq:seq + 1], cache, table[seq:seq + 1], _int([last * PAGE]))[0]
+        assert torch.allclose(got.float(), ref.float(), rtol=2.0 ** -6, atol=2.0 ** -9 * float(v.abs().max()))
+    assert torch.equal(G.kv4_attention(q, cache, table, _int(lens)), want)
+
+
+def test_kv4_attention_after_the_error_stops():
+    lens, cache, table, q, _, _ = _attention_inputs(7)
+    st, out = G.new_status(_dev()), torch.full_like(q, 7.0)
+    bad = list(lens)
+    bad[3] = -5
+    G.kv4_attention(q, cache, table, _int(bad), status=st)
+    for _ in range(2):
+        G.kv4_attention(q, cache, table, _int(lens), out=out, status=st)
+        assert (out == 7).all()
+    assert G.status_read(st) == (INVALID, 3)
