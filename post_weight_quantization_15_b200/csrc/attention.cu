@@ -247,7 +247,7 @@ __device__ __forceinline__ Work find_work(const AttentionArgs& A, int slot, int 
       k0 = A.cu_k[b];
       k1 = A.cu_k[b + 1];
       if (q0 < 0 || q1 < q0 || q1 > A.total_q || k0 < 0 || k1 < k0 || k1 > A.total_k)
-        set_error(st, GPTQ_ERR_INVALID_ARG, b, STAGE_ATTENTION);
+        set_own_error(st, A.launch, GPTQ_ERR_INVALID_ARG, b, STAGE_ATTENTION);
       else
         pairs = (int)((((int64_t)(q1 - q0) << A.packed) + 2 * TQ - 1) / (2 * TQ));
     }
@@ -474,7 +474,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
   int b0 = 0, base = 0;
   if (warp == 8) w = find_work(A, at / packs, at % packs, b0, base, st);
   if (warp == 0 && lane == 0) {
-    S.skip = has_error(st);
+    S.skip = stopped(st, A.launch);
     S.abort = 0;
     S.q_armed[0] = S.q_armed[1] = S.kv_armed = S.committed = 0;
     S.mine.pair = -1;
@@ -901,6 +901,7 @@ int head_map(CUtensorMap* map, CUtensorMapDataType dt, const void* p, int tokens
 int launch_attention(const AttentionArgs& args, int dtype, int32_t* st, cudaStream_t s) {
   AttentionArgs A = args;
   A.packed = packed_heads(A);
+  A.launch = next_launch();
   CUtensorMap tq, tk, tv;
   const CUtensorMapDataType dt = dtype == GPTQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   int rc = head_map(&tq, dt, A.q, A.total_q, A.heads_q, A.head_dim, A.q_ts, A.q_hs, A.packed);

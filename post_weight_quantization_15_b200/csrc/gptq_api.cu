@@ -362,7 +362,7 @@ int gptq_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
     return GPTQ_ERR_INVALID_ARG;
   const AttentionArgs A{q, k, v, o, q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride,
                         v_head_stride, o_token_stride, o_head_stride, cu_q, cu_k, count, total_q, total_k, heads_q,
-                        heads_kv, head_dim, scale, causal, 0};
+                        heads_kv, head_dim, scale, causal, 0, 0};
   return launch_attention(A, dtype, d_status, as_stream(stream));
 }
 

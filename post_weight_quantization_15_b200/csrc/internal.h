@@ -144,6 +144,7 @@ struct AttentionArgs {
   float scale;
   int causal;
   int packed;                             // log2 of the query heads that share a tile (set by the launch)
+  int launch;                             // the call's number, for the errors it records (likewise)
 };
 int launch_attention(const AttentionArgs& A, int dtype, int32_t* st, cudaStream_t s);
 // The 4-bit cache: [0] keys, [1] values (layout in kv4.cuh).

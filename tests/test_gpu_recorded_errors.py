@@ -220,3 +220,30 @@ def test_kv4_attention_after_the_error_stops():
         G.kv4_attention(q, cache, table, _int(lens), out=out, status=st)
         assert (out == 7).all()
     assert G.status_read(st) == (INVALID, 3)
+
+
+# --------------------------------------------------------------------------- #
+# attention: pairs of tiles for every SM several times over, and shared ones
+# --------------------------------------------------------------------------- #
+@pytest.mark.parametrize("which", ["queries", "keys"])
+@pytest.mark.parametrize("lens,past,hq,hk,at", [([150] * 300, 10, 8, 2, 1), ([600] * 40, 0, 4, 4, 20),
+                                                 ([1, 3, 2, 1], 4000, 4, 1, 2)])
+def test_attention_beside_bad_bounds(lens, past, hq, hk, at, which):
+    """A bound that is out of range takes the two sequences beside it, and no other."""
+    rng = np.random.default_rng(8)
+    cu_q, cu_k = _cu(lens), _cu([n + past for n in lens])
+    q = _rand(rng, (cu_q[-1], hq, 64), HF)
+    k, v = (_rand(rng, (cu_k[-1], hk, 64), HF) for _ in range(2))
+    want = G.attention(q, k, v, _int(cu_q), _int(cu_k))
+    rows = slice(cu_q[at - 1], cu_q[at + 1])
+    (cu_q if which == "queries" else cu_k)[at] = -3
+    for _ in range(3):
+        st, out = G.new_status(_dev()), torch.full_like(q, 7.0)
+        G.attention(q, k, v, _int(cu_q), _int(cu_k), out=out, status=st)
+        code, seq = G.status_read(st)
+        assert code == INVALID and seq in (at - 1, at)
+        assert (out[rows] == 7).all()
+        out[rows] = want[rows]
+        assert torch.equal(out, want)
+    G.attention(q, k, v, _int(cu_q), _int(cu_k), out=out.fill_(5.0), status=st)      # the error is an earlier call's
+    assert (out == 5).all()
