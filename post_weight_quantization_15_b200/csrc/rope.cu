@@ -39,6 +39,7 @@ struct RopeArgs {
   void* q;
   void* k;
   void* v;
+  int launch;                             // the call's number, for the errors it records
 };
 
 template <int W, typename T>
@@ -60,7 +61,7 @@ __device__ __forceinline__ void storew(T* p, const float (&v)[W]) {
 template <typename TX, typename TO, int W, bool BIAS>
 __global__ void __launch_bounds__(THREADS, W == 8 ? 4 : 5)
 rope_qkv_kernel(const __grid_constant__ RopeArgs A, int units, int subs, int per, int per_block, int32_t* st) {
-  if (has_error(st)) return;
+  if (stopped(st, A.launch)) return;       // (threads work by themselves)
   const int turned = A.hq + A.hk, heads = turned + A.hk;
   const int sub = (int)threadIdx.x / units % subs, own = (int)threadIdx.x / (units * subs);
   const int t = (int)blockIdx.x * per + own;
@@ -68,7 +69,8 @@ rope_qkv_kernel(const __grid_constant__ RopeArgs A, int units, int subs, int per
   if (own >= per || t >= A.tokens) return;
   int pos = A.positions != nullptr ? A.positions[t] : t;
   if (A.rot > 0 && (pos < 0 || pos >= A.max_pos)) {
-    if (threadIdx.x % (units * subs) == 0 && blockIdx.y == 0) set_error(st, GPTQ_ERR_INVALID_ARG, t, STAGE_ROPE);
+    if (threadIdx.x % (units * subs) == 0 && blockIdx.y == 0)
+      set_own_error(st, A.launch, GPTQ_ERR_INVALID_ARG, t, STAGE_ROPE);
     pos = 0;
   }
   for (int j = (int)threadIdx.x % units; j < units; j += THREADS) {      // (a head may have more pieces than the block threads)
@@ -170,7 +172,7 @@ bool al16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 int launch_rope_qkv(const void* X, int x_dtype, int64_t ld, const float* bias, const float* cos, const float* sin,
                     int max_pos, int rot, int interleaved, const int32_t* positions, int tokens, int hq, int hk,
                     int d, int out_dtype, void* q, void* k, void* v, int32_t* st, cudaStream_t s) {
-  RopeArgs A{X, ld, bias, cos, sin, positions, max_pos, rot, interleaved, tokens, hq, hk, d, q, k, v};
+  RopeArgs A{X, ld, bias, cos, sin, positions, max_pos, rot, interleaved, tokens, hq, hk, d, q, k, v, next_launch()};
   const int xb = x_dtype == GPTQ_F32 ? 4 : 2;
   const bool al = al16(X) && (ld * xb) % 16 == 0 && al16(q) && al16(k) && al16(v) && (rot == 0 || (al16(cos) && al16(sin))) &&
                   (bias == nullptr || al16(bias));

@@ -247,3 +247,27 @@ def test_attention_beside_bad_bounds(lens, past, hq, hk, at, which):
         assert torch.equal(out, want)
     G.attention(q, k, v, _int(cu_q), _int(cu_k), out=out.fill_(5.0), status=st)      # the error is an earlier call's
     assert (out == 5).all()
+
+
+# --------------------------------------------------------------------------- #
+# rope_qkv
+# --------------------------------------------------------------------------- #
+@pytest.mark.parametrize("tokens,hq,hk,d,dt", [(20000, 4, 1, 64, FF), (3000, 32, 8, 128, BF), (9001, 2, 2, 20, HF),
+                                               (2000, 1, 1, 600, FF)])
+@pytest.mark.parametrize("bad", [-1, 500])
+def test_rope_qkv_beside_a_bad_position(tokens, hq, hk, d, dt, bad):
+    """A position outside the tables is read as 0, in blocks that start after it was recorded too."""
+    rng = np.random.default_rng(9)
+    X = _rand(rng, (tokens, (hq + 2 * hk) * d), dt)
+    cos, sin = (_rand(rng, (500, d // 2), FF) for _ in range(2))
+    pos = torch.arange(tokens, dtype=torch.int32, device=_dev()) % 500
+    pos[1] = pos[tokens - 2] = 0
+    want = G.rope_qkv(X, cos, sin, hq, hk, d, positions=pos)
+    pos[1] = pos[tokens - 2] = bad
+    for _ in range(3):
+        st = G.new_status(_dev())
+        got = G.rope_qkv(X, cos, sin, hq, hk, d, positions=pos, status=st)
+        code, token = G.status_read(st)
+        assert code == INVALID and token in (1, tokens - 2)
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
