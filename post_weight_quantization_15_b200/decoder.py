@@ -134,6 +134,51 @@ def quantize_decoder_blocks(X0: torch.Tensor, cu: torch.Tensor, blocks: Sequence
     return out, X
 
 
+@dataclasses.dataclass
+class _Past:
+    """Where a continued batch's keys lie when the cached ones come before them."""
+    cu_k: torch.Tensor             # int32 [sequences + 1]: cached and new keys of each sequence
+    total: int
+    new: torch.Tensor              # the new tokens' rows among them
+    first: int                     # the first and last + 1 of the batch's tokens that a sequence has
+    last: int
+
+
+def _past(cu: torch.Tensor, start: torch.Tensor, table: torch.Tensor, capacity: int, tokens: int) -> Optional[_Past]:
+    """None if no sequence has anything before its new tokens.  Reads cu and start back."""
+    n = cu.numel() - 1
+    B._ints(cu, (n + 1,), "cu")
+    B._ints(start, (n,), "start")
+    B._table(table, n)
+    c0, c1, s0 = torch.stack([cu[:-1], cu[1:], start]).tolist()
+    if any(a < 0 or b < a or b > tokens for a, b in zip(c0, c1)):
+        raise ValueError("cu must be non-decreasing rows of X")
+    if any(s < 0 or s + b - a > capacity for a, b, s in zip(c0, c1, s0)):
+        raise ValueError("a sequence's positions do not fit its row of the table")
+    s0 = [s if b > a else 0 for a, b, s in zip(c0, c1, s0)]           # (without a query nothing is read)
+    if not any(s0):
+        return None
+    ends = [0]
+    for a, b, s in zip(c0, c1, s0):
+        ends.append(ends[-1] + s + b - a)
+    if ends[-1] > 2 ** 31 - 1:
+        raise ValueError("the sequences and what precedes them have more than 2^31 - 1 tokens")
+    lens = torch.tensor([b - a for a, b in zip(c0, c1)], device=cu.device)
+    shift = torch.tensor([e + s - a for e, s, a in zip(ends, s0, c0)], device=cu.device)
+    new = torch.arange(c0[0], c1[-1], device=cu.device) + shift.repeat_interleave(lens, output_size=c1[-1] - c0[0])
+    return _Past(torch.tensor(ends, dtype=torch.int32, device=cu.device), ends[-1], new, c0[0], c1[-1])
+
+
+def _attend(q, k, v, cu, cache, table, past: Optional[_Past], status) -> torch.Tensor:
+    """Attention of the new tokens over themselves, and over what the cache holds before them."""
+    if past is None:
+        return B.attention(q, k, v, cu, status=status)
+    held = B.kv4_read(cache, table, past.cu_k, past.total, dtype=k.dtype, status=status)
+    for h, x in zip(held, (k, v)):                 # the new ones as they are, as in a prompt from position 0
+        h[past.new] = x[past.first:past.last]
+    return B.attention(q, *held, cu, past.cu_k, status=status)
+
+
 def prompt_blocks(X: torch.Tensor, cu: torch.Tensor, blocks: Sequence[QuantizedBlock], rotary: Rotary,
                   positions: Optional[torch.Tensor] = None, caches: Optional[Sequence[B.KV4Cache]] = None,
                   table: Optional[torch.Tensor] = None, start: Optional[torch.Tensor] = None,
@@ -141,12 +186,18 @@ def prompt_blocks(X: torch.Tensor, cu: torch.Tensor, blocks: Sequence[QuantizedB
     """A packed batch of prompts, bf16 [tokens, d], through the blocks; returns the stream after them.
 
     caches (one per block): the prompts' keys and values are appended at positions start[b] ...
-    (int32 [sequences]; None: 0) of sequence b, in the pages that table names.
+    (int32 [sequences]; None: 0) of sequence b, in the pages that table names, and the tokens attend
+    to the cached positions before them too (a prompt in chunks, the next turn of a conversation).
+    With start given, cu and start are read back: not inside a stream capture.
     """
     _check_stream(X)
     if caches is not None and (table is None or len(caches) != len(blocks)):
         raise ValueError("caches need a table, and one cache per block")
-    r, y = rotary, None
+    if start is not None and caches is None:
+        raise ValueError("start belongs to caches")
+    r, y, past = rotary, None, None
+    if start is not None and blocks:
+        past = _past(cu, start, table, table.shape[1] * caches[0].k_codes.shape[2], X.shape[0])
     if caches is not None and start is None:
         start = torch.zeros(cu.numel() - 1, dtype=torch.int32, device=X.device)
     for i, b in enumerate(blocks):
@@ -155,7 +206,7 @@ def prompt_blocks(X: torch.Tensor, cu: torch.Tensor, blocks: Sequence[QuantizedB
                              interleaved=r.interleaved, status=status)
         if caches is not None:
             B.kv4_append(caches[i], k, v, table, cu, start, status=status)
-        a = B.attention(q, k, v, cu, status=status).flatten(1)
+        a = _attend(q, k, v, cu, caches[i] if past else None, table, past, status).flatten(1)
         X, h = B.add_norm(X, b.norm_mlp, Y=_forward(b.o, a, status), eps=b.eps, status=status)
         y = _forward(b.down, _mlp_hidden(b.gate_up, h, status), status)
     return X if y is None else G.residual_add(X, y, status)

@@ -1,0 +1,104 @@
+"""Prompts through quantized blocks into the 4-bit cache where the call's defaults and the batch's shape
+matter: continued prompts, positions, what is reported, rows that no sequence has."""
+import numpy as np
+import pytest
+
+from oracle import block_oracle as B
+from tests.test_gpu_block import BF, U, _attn_tol, _close, _cu, _dev, _int, _np
+from tests.test_gpu_decoder import EPS, HD, HK, HQ, TABLE, _caches, _positions, _stream_of, quantized  # noqa: F401
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import post_weight_quantization_15_b200 as G
+    from post_weight_quantization_15_b200 import decoder as D
+
+TENSORS = ("k_codes", "k_params", "v_codes", "v_params")
+
+
+def _rows(n, seed):
+    return _stream_of(-(-n // 8) * 8, seed)[:n].contiguous()
+
+
+def _forward(q, X):
+    return G.linear_bf16(X, G.dequantize(q, BF))
+
+
+def _mlp(b, h):
+    w = G.dequantize(b.gate_up, BF)
+    f = w.shape[0] // 2
+    return _forward(b.down, G.silu_mul(G.linear_bf16(h, w[:f].contiguous()), G.linear_bf16(h, w[f:].contiguous())))
+
+
+def _explicit(x, lens, start, blocks, rot, caches, table):
+    """The operators one by one, the keys put together sequence by sequence; the attention against the oracle."""
+    cu, after = _cu(lens), [s + n if n else 0 for s, n in zip(start, lens)]
+    before, cu_k = [s if n else 0 for s, n in zip(start, lens)], _cu(after)
+    pos = _int(np.concatenate([s + np.arange(n) for s, n in zip(start, lens)]).tolist())
+    y = None
+    for b, c in zip(blocks, caches):
+        x, h = G.add_norm(x, b.norm_attn, Y=y, eps=EPS)
+        q, k, v = G.rope_qkv(_forward(b.qkv, h), rot.cos, rot.sin, HQ, HK, HD, positions=pos)
+        old = G.kv4_read(c, table, _int(_cu(before)), sum(before))
+        cb = _cu(before)
+        both = [torch.cat([t for i in range(len(lens)) for t in (o[cb[i]:cb[i + 1]], z[cu[i]:cu[i + 1]])])
+                for o, z in zip(old, (k, v))]
+        G.kv4_append(c, k, v, table, _int(cu), _int(start))
+        a = G.attention(q, *both, _int(cu), _int(cu_k))
+        ref, tol = _attn_tol(_np(q), *(_np(t) for t in both), cu, cu_k, HD ** -0.5, True, BF, U[BF])
+        _close(a, ref, tol, "a")
+        x, h = G.add_norm(x, b.norm_mlp, Y=_forward(b.o, a.flatten(1)), eps=EPS)
+        y = _mlp(b, h)
+    return G.residual_add(x, y)
+
+
+@pytest.mark.parametrize("lens,start", [([20, 33, 1], [37, 0, 90]), ([5, 0, 38], [0, 64, 90]), ([1, 1, 1], [31, 32, 95]),
+                                        ([0, 0, 9], [10, 20, 30])])
+def test_a_prompt_goes_on_behind_what_the_cache_holds(quantized, lens, start):  # noqa: F811
+    blocks, rot, _ = quantized
+    table = _int(TABLE)
+    caches, kept = _caches(2), _caches(2)
+    first = _rows(sum(start), 31)
+    for c in (caches, kept):
+        D.prompt_blocks(first, _int(_cu(start)), blocks, rot, positions=_positions(start), caches=c, table=table)
+    x = _rows(sum(lens), 32)
+    pos = _int(np.concatenate([s + np.arange(n) for s, n in zip(start, lens)]).tolist())
+    got = D.prompt_blocks(x, _int(_cu(lens)), blocks, rot, positions=pos, caches=caches, table=table, start=_int(start))
+    want = _explicit(x, lens, start, blocks, rot, kept, table)
+    assert torch.equal(got, want)
+    for a, b in zip(caches, kept):
+        for n in TENSORS:
+            assert torch.equal(getattr(a, n), getattr(b, n)), n
+
+
+def test_a_start_of_zero_is_no_start(quantized):  # noqa: F811
+    blocks, rot, _ = quantized
+    lens, table = [37, 0, 90], _int(TABLE)
+    x, pos = _rows(127, 33), _positions([37, 0, 90])
+    outs, caches = [], []
+    for start in (None, _int([0, 0, 0]), _int([0, 55, 0])):      # (a sequence without new tokens has nothing to see)
+        caches.append(_caches(2))
+        outs.append(D.prompt_blocks(x, _int(_cu(lens)), blocks, rot, positions=pos, caches=caches[-1], table=table,
+                                    start=start))
+    for o, c in zip(outs[1:], caches[1:]):
+        assert torch.equal(o, outs[0])
+        for a, b in zip(c, caches[0]):
+            assert all(torch.equal(getattr(a, n), getattr(b, n)) for n in TENSORS)
+
+
+def test_continued_prompt_refusals(quantized):  # noqa: F811
+    blocks, rot, _ = quantized
+    x, table = _rows(6, 34), _int(TABLE)
+    cu, pos = _int([0, 2, 4, 6]), _int([0, 1] * 3)
+    for start in ([0, -1, 0], [0, 127, 0]):                      # (TABLE: 128 positions)
+        caches = _caches(2)
+        with pytest.raises(ValueError, match="positions"):
+            D.prompt_blocks(x, cu, blocks, rot, pos, caches, table, _int(start))
+        assert not any(c.k_codes.any() for c in caches)
+    with pytest.raises(ValueError, match="start"):
+        D.prompt_blocks(x, cu, blocks, rot, pos, start=_int([0, 0, 0]))
+    with pytest.raises(ValueError, match="start"):
+        D.prompt_blocks(x, cu, blocks, rot, pos, _caches(2), table, _int([0, 0]))
+    with pytest.raises(ValueError, match="cu"):
+        D.prompt_blocks(x, _int([0, 2, 4, 7]), blocks, rot, pos, _caches(2), table, _int([0, 0, 1]))
