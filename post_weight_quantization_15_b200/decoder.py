@@ -134,6 +134,18 @@ def quantize_decoder_blocks(X0: torch.Tensor, cu: torch.Tensor, blocks: Sequence
     return out, X
 
 
+def _positions(cu: torch.Tensor, start: Optional[torch.Tensor], tokens: int) -> torch.Tensor:
+    """Each row's position inside its sequence, behind start[b]; 0 for a row of no sequence."""
+    if cu.numel() < 2:
+        return torch.zeros(tokens, dtype=torch.int32, device=cu.device)
+    t = torch.arange(tokens, dtype=torch.int32, device=cu.device)
+    b = torch.searchsorted(cu, t, right=True) - 1                     # the last sequence that begins by row t
+    inside = (b >= 0) & (b < cu.numel() - 1)
+    b = b.clamp(0, cu.numel() - 2)
+    pos = t - cu[b] if start is None else t - cu[b] + start[b]
+    return torch.where(inside, pos, 0)
+
+
 @dataclasses.dataclass
 class _Past:
     """Where a continued batch's keys lie when the cached ones come before them."""
@@ -185,6 +197,8 @@ def prompt_blocks(X: torch.Tensor, cu: torch.Tensor, blocks: Sequence[QuantizedB
                   status: Optional[torch.Tensor] = None) -> torch.Tensor:
     """A packed batch of prompts, bf16 [tokens, d], through the blocks; returns the stream after them.
 
+    positions int32 [tokens] for the rotary tables; None: those inside the sequences, row cu[b] + i at
+    start[b] + i, as decode_blocks counts on.
     caches (one per block): the prompts' keys and values are appended at positions start[b] ...
     (int32 [sequences]; None: 0) of sequence b, in the pages that table names, and the tokens attend
     to the cached positions before them too (a prompt in chunks, the next turn of a conversation).
@@ -200,6 +214,9 @@ def prompt_blocks(X: torch.Tensor, cu: torch.Tensor, blocks: Sequence[QuantizedB
         past = _past(cu, start, table, table.shape[1] * caches[0].k_codes.shape[2], X.shape[0])
     if caches is not None and start is None:
         start = torch.zeros(cu.numel() - 1, dtype=torch.int32, device=X.device)
+    if positions is None and r.cos is not None:
+        B._ints(cu, (cu.numel(),), "cu")
+        positions = _positions(cu, start, X.shape[0])
     for i, b in enumerate(blocks):
         X, h = B.add_norm(X, b.norm_attn, Y=y, eps=b.eps, status=status)
         q, k, v = B.rope_qkv(_forward(b.qkv, h, status), r.cos, r.sin, r.heads_q, r.heads_kv, r.head_dim, positions,

@@ -38,3 +38,12 @@ def test_types_of_a_continued_batch():
             D._past(cu, start, TABLE, 128, 5)
     with pytest.raises(ValueError, match="table"):
         D._past(_i(0, 2, 3, 5), _i(0, 0, 1), TABLE[:2], 128, 5)
+
+
+def test_positions_inside_the_sequences():
+    cu = _i(0, 3, 3, 5)
+    assert D._positions(cu, None, 7).tolist() == [0, 1, 2, 0, 1, 0, 0]       # (rows 5 and 6 have no sequence)
+    assert D._positions(cu, _i(10, 5, 1), 5).tolist() == [10, 11, 12, 1, 2]
+    assert D._positions(_i(2, 4), _i(7), 6).tolist() == [0, 0, 7, 8, 0, 0]
+    assert D._positions(cu, None, 7).dtype == torch.int32 and D._positions(_i(0), None, 2).tolist() == [0, 0]
+    assert D._positions(_i(0, 0, 0), _i(3, 4), 0).shape == (0,)

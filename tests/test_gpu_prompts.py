@@ -102,3 +102,23 @@ def test_continued_prompt_refusals(quantized):  # noqa: F811
         D.prompt_blocks(x, cu, blocks, rot, pos, _caches(2), table, _int([0, 0]))
     with pytest.raises(ValueError, match="cu"):
         D.prompt_blocks(x, _int([0, 2, 4, 7]), blocks, rot, pos, _caches(2), table, _int([0, 0, 1]))
+
+
+@pytest.mark.parametrize("lens,start", [([37, 0, 90], None), ([20, 33, 1], [37, 0, 90])])
+def test_positions_follow_from_the_sequences(quantized, lens, start):  # noqa: F811
+    """Without positions a token is at its place in its own sequence, in the cache too."""
+    blocks, rot, _ = quantized
+    table, x = _int(TABLE), _rows(sum(lens), 35)
+    pos = _int(np.concatenate([s + np.arange(n) for s, n in zip(start or [0] * 3, lens)]).tolist())
+    results = []
+    for p in (pos, None):
+        caches = _caches(2)
+        if start:
+            D.prompt_blocks(_rows(sum(start), 36), _int(_cu(start)), blocks, rot, positions=_positions(start),
+                            caches=caches, table=table)
+        results.append((D.prompt_blocks(x, _int(_cu(lens)), blocks, rot, p, caches, table,
+                                        _int(start) if start else None), caches))
+    (a, ca), (b, cb) = results
+    assert torch.equal(a, b)
+    for c, d in zip(ca, cb):
+        assert all(torch.equal(getattr(c, n), getattr(d, n)) for n in TENSORS)
