@@ -88,6 +88,14 @@ def _mlp_hidden(gate_up: G.QuantizedLayer, h: torch.Tensor, st) -> torch.Tensor:
     return G.silu_mul(G.linear_bf16(h, What[:f], st), G.linear_bf16(h, What[f:], st), st)
 
 
+def _watched(status: Optional[torch.Tensor], X: torch.Tensor):
+    """(status block, whether the call made it and has to read it); none inside a stream capture, where nothing
+    can be read back."""
+    if status is not None or torch.cuda.is_current_stream_capturing():
+        return status, False
+    return G.new_status(X.device), True
+
+
 def _check_stream(X: torch.Tensor):
     if X.dim() != 2 or X.dtype != torch.bfloat16 or not X.is_contiguous():
         raise ValueError("X must be a contiguous bf16 [tokens, d] tensor")
@@ -203,10 +211,14 @@ def prompt_blocks(X: torch.Tensor, cu: torch.Tensor, blocks: Sequence[QuantizedB
     (int32 [sequences]; None: 0) of sequence b, in the pages that table names, and the tokens attend
     to the cached positions before them too (a prompt in chunks, the next turn of a conversation).
     With start given, cu and start are read back: not inside a stream capture.
+
+    status: the caller's status block, read by the caller.  None: errors found on the device (a position outside
+    the tables, a group that is not finite, ...) are waited for and raised, except inside a stream capture.
     """
     _check_stream(X)
     if caches is not None and (table is None or len(caches) != len(blocks)):
         raise ValueError("caches need a table, and one cache per block")
+    status, own = _watched(status, X)
     if start is not None and caches is None:
         raise ValueError("start belongs to caches")
     r, y, past = rotary, None, None
@@ -226,7 +238,10 @@ def prompt_blocks(X: torch.Tensor, cu: torch.Tensor, blocks: Sequence[QuantizedB
         a = _attend(q, k, v, cu, caches[i] if past else None, table, past, status).flatten(1)
         X, h = B.add_norm(X, b.norm_mlp, Y=_forward(b.o, a, status), eps=b.eps, status=status)
         y = _forward(b.down, _mlp_hidden(b.gate_up, h, status), status)
-    return X if y is None else G.residual_add(X, y, status)
+    out = X if y is None else G.residual_add(X, y, status)
+    if own:
+        G.raise_on_status(status, "prompt_blocks")
+    return out
 
 
 def decode_blocks(X: torch.Tensor, lengths: torch.Tensor, blocks: Sequence[QuantizedBlock], rotary: Rotary,
@@ -237,6 +252,7 @@ def decode_blocks(X: torch.Tensor, lengths: torch.Tensor, blocks: Sequence[Quant
     lengths int32 [sequences]: tokens of each sequence in the caches before this one, which is the
     new token's position too; it is appended and attended to.  lengths itself is not advanced.
     At most 16 sequences (qmatvec's rows).  ws: kv4_attention's workspace (a captured step needs its own).
+    status: as prompt_blocks's; steps that should not be waited for one by one, and captured ones, take one.
     """
     _check_stream(X)
     n = X.shape[0]
@@ -246,6 +262,7 @@ def decode_blocks(X: torch.Tensor, lengths: torch.Tensor, blocks: Sequence[Quant
         raise ValueError("decode_blocks needs one cache per block")
     if lengths.dtype != torch.int32 or tuple(lengths.shape) != (n,):
         raise ValueError("lengths must be int32 [sequences]")
+    status, own = _watched(status, X)
     r, y = rotary, None
     cu = torch.arange(n + 1, dtype=torch.int32, device=X.device)
     after = lengths + 1
@@ -259,4 +276,7 @@ def decode_blocks(X: torch.Tensor, lengths: torch.Tensor, blocks: Sequence[Quant
         gu = G.qmatvec(b.gate_up, h, status)
         f = gu.shape[1] // 2
         y = G.qmatvec(b.down, G.silu_mul(gu[:, :f].contiguous(), gu[:, f:].contiguous(), status), status)
-    return X if y is None else G.residual_add(X, y, status)
+    out = X if y is None else G.residual_add(X, y, status)
+    if own:
+        G.raise_on_status(status, "decode_blocks")
+    return out

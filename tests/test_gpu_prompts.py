@@ -122,3 +122,33 @@ def test_positions_follow_from_the_sequences(quantized, lens, start):  # noqa: F
     assert torch.equal(a, b)
     for c, d in zip(ca, cb):
         assert all(torch.equal(getattr(c, n), getattr(d, n)) for n in TENSORS)
+
+
+def test_errors_on_the_device_are_raised(quantized):  # noqa: F811
+    """Without a status block of the caller's nothing goes wrong in silence; with one it is recorded there."""
+    blocks, rot, _ = quantized
+    x, table, short = _rows(3, 39), _int(TABLE), _int([t[:1] for t in TABLE])
+    nan = x.clone()
+    nan[1, 5] = float("nan")
+    far = _int([0, 5000, 0])                                     # (the tables end at 2048)
+
+    def step(x, lengths, table, **kw):
+        return D.decode_blocks(x, _int(lengths), blocks, rot, _caches(2), table, **kw)
+
+    def prompt(x, table, positions=None, **kw):
+        return D.prompt_blocks(x, _int([0, 1, 2, 3]), blocks, rot, positions, _caches(2), table, **kw)
+
+    inv, nonf = G.gptq.ERR_INVALID_ARG, G.gptq.ERR_NONFINITE
+    for code, call in ((inv, lambda **kw: step(x, [0, 32, 0], short, **kw)),      # no page for the new token
+                       (inv, lambda **kw: step(x, [0, 5000, 0], table, **kw)),
+                       (nonf, lambda **kw: step(nan, [0, 0, 0], table, **kw)),
+                       (inv, lambda **kw: prompt(x, table, far, **kw)),
+                       (inv, lambda **kw: prompt(x, _int([[0], [-1], [1]]), **kw)),
+                       (nonf, lambda **kw: prompt(nan, table, **kw))):
+        with pytest.raises(G.GptqError) as e:
+            call()
+        assert e.value.code == code
+        st = G.new_status(_dev())
+        call(status=st)
+        assert G.status_read(st) == (code, 1)
+    assert torch.isfinite(step(x, [0, 1, 2], table)).all() and torch.isfinite(prompt(x, table)).all()
