@@ -88,6 +88,15 @@ def _mlp_hidden(gate_up: G.QuantizedLayer, h: torch.Tensor, st) -> torch.Tensor:
     return G.silu_mul(G.linear_bf16(h, What[:f], st), G.linear_bf16(h, What[f:], st), st)
 
 
+def _without_strays(X: torch.Tensor, cu: torch.Tensor) -> torch.Tensor:
+    """X with the rows of no sequence (before cu[0], from cu[-1] on) as 0."""
+    B._ints(cu, (cu.numel(),), "cu")
+    if cu.numel() < 2:
+        return torch.zeros_like(X)
+    t = torch.arange(X.shape[0], dtype=torch.int32, device=X.device)
+    return torch.where(((t >= cu[0]) & (t < cu[-1]))[:, None], X, 0)
+
+
 def _watched(status: Optional[torch.Tensor], X: torch.Tensor):
     """(status block, whether the call made it and has to read it); none inside a stream capture, where nothing
     can be read back."""
@@ -111,7 +120,8 @@ def quantize_decoder_blocks(X0: torch.Tensor, cu: torch.Tensor, blocks: Sequence
     """Quantize decoder blocks in sequence; returns (the blocks, the last block's output).
 
     X0 bf16 [tokens, d] (tokens a multiple of 8), the packed calibration sequences; cu int32
-    [sequences + 1] their first rows and the end; positions int32 [tokens] for the rotary tables
+    [sequences + 1] their first rows and the end (rows of no sequence, such as those that pad the batch to a
+    multiple of 8, take no part in the calibration and come out as 0); positions int32 [tokens] for the rotary tables
     (None: row t is at position t).  decode_blocks takes desc_act blocks too, more slowly (qmatvec
     reads their groups column by column).
     """
@@ -119,7 +129,7 @@ def quantize_decoder_blocks(X0: torch.Tensor, cu: torch.Tensor, blocks: Sequence
     st = status if status is not None else G.new_status(X0.device)
     how = (bits, group_size, sym, desc_act, damp_percent, st)
     r = rotary
-    x, y = X0, None                # the stream, and what is still to be added to it
+    x, y = _without_strays(X0, cu), None   # the stream, and what is still to be added to it
     out: List[QuantizedBlock] = []
     for w in blocks:
         x, h = B.add_norm(x, w.norm_attn, Y=y, eps=eps, status=st)
@@ -127,7 +137,8 @@ def quantize_decoder_blocks(X0: torch.Tensor, cu: torch.Tensor, blocks: Sequence
         qkv, perm_qkv = _quantize([w.wq, w.wk, w.wv], h, *how)
         q, k, v = B.rope_qkv(_forward(qkv, h, st), r.cos, r.sin, r.heads_q, r.heads_kv, r.head_dim, positions,
                              interleaved=r.interleaved, status=st)
-        a = B.attention(q, k, v, cu, status=st).flatten(1)
+        # (attention leaves rows of no sequence as they are: 0, where the Hessian of o must not see them)
+        a = B.attention(q, k, v, cu, out=torch.zeros_like(q), status=st).flatten(1)
         o, perm_o = _quantize([w.wo], a, *how)
         x_mid, h2 = B.add_norm(x, w.norm_mlp, Y=_forward(o, a, st), eps=eps, status=st)
         gate_up, perm_gate_up = _quantize([w.w_gate, w.w_up], h2, *how)
@@ -191,12 +202,13 @@ def _past(cu: torch.Tensor, start: torch.Tensor, table: torch.Tensor, capacity: 
 
 def _attend(q, k, v, cu, cache, table, past: Optional[_Past], status) -> torch.Tensor:
     """Attention of the new tokens over themselves, and over what the cache holds before them."""
+    o = torch.zeros_like(q)                        # rows of no sequence attend to nothing
     if past is None:
-        return B.attention(q, k, v, cu, status=status)
+        return B.attention(q, k, v, cu, out=o, status=status)
     held = B.kv4_read(cache, table, past.cu_k, past.total, dtype=k.dtype, status=status)
     for h, x in zip(held, (k, v)):                 # the new ones as they are, as in a prompt from position 0
         h[past.new] = x[past.first:past.last]
-    return B.attention(q, *held, cu, past.cu_k, status=status)
+    return B.attention(q, *held, cu, past.cu_k, out=o, status=status)
 
 
 def prompt_blocks(X: torch.Tensor, cu: torch.Tensor, blocks: Sequence[QuantizedBlock], rotary: Rotary,

@@ -47,3 +47,14 @@ def test_positions_inside_the_sequences():
     assert D._positions(_i(2, 4), _i(7), 6).tolist() == [0, 0, 7, 8, 0, 0]
     assert D._positions(cu, None, 7).dtype == torch.int32 and D._positions(_i(0), None, 2).tolist() == [0, 0]
     assert D._positions(_i(0, 0, 0), _i(3, 4), 0).shape == (0,)
+
+
+def test_rows_of_no_sequence_are_cleared():
+    x = torch.full((6, 2), float("nan"))
+    x[1:4] = torch.tensor([[1.0, -0.0], [2.0, 3.0], [float("inf"), 4.0]])
+    y = D._without_strays(x, _i(1, 3, 4))
+    assert torch.equal(y[1:4], x[1:4]) and (y[[0, 4, 5]] == 0).all()
+    assert torch.equal(D._without_strays(x[1:4], _i(0, 3)), x[1:4])
+    assert (D._without_strays(x, _i(0)) == 0).all() and (D._without_strays(x, _i(2, 2)) == 0).all()
+    with pytest.raises(ValueError, match="cu"):
+        D._without_strays(x, _i(0, 3).long())

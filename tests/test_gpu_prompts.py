@@ -5,7 +5,8 @@ import pytest
 
 from oracle import block_oracle as B
 from tests.test_gpu_block import BF, U, _attn_tol, _close, _cu, _dev, _int, _np
-from tests.test_gpu_decoder import EPS, HD, HK, HQ, TABLE, _caches, _positions, _stream_of, quantized  # noqa: F401
+from tests.test_gpu_decoder import (  # noqa: F401
+    EPS, HD, HK, HQ, TABLE, _caches, _positions, _rotary, _stream_of, _weights, quantized)
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -152,3 +153,42 @@ def test_errors_on_the_device_are_raised(quantized):  # noqa: F811
         call(status=st)
         assert G.status_read(st) == (code, 1)
     assert torch.isfinite(step(x, [0, 1, 2], table)).all() and torch.isfinite(prompt(x, table)).all()
+
+
+def test_rows_of_no_sequence_take_no_part_in_the_calibration():
+    """A batch padded to a multiple of 8: whatever the padding holds, the layers are those of zeros there, and
+    every product's input is 0 in those rows (so the Hessians are the sequences' alone)."""
+    cu, pos = _int([0, 600, 997]), _positions([600, 397, 27])
+    results = []
+    for pad in (0.0, 3.0, float("nan")):
+        x = _stream_of(1024, 40)
+        x[997:] = pad
+        blocks, out = D.quantize_decoder_blocks(x, cu, [_weights(5), _weights(6)], _rotary(), positions=pos, eps=EPS,
+                                                record=True)
+        assert (out[997:] == 0).all() and torch.isfinite(out).all()
+        for b in blocks:
+            for n in ("h", "a", "h_mlp", "m"):
+                assert (b.stages[n][997:] == 0).all() and b.stages[n][:997].any(), n
+        results.append((blocks, out))
+    for blocks, out in results[1:]:
+        assert torch.equal(out, results[0][1])
+        for a, b in zip(blocks, results[0][0]):
+            for layer in ("qkv", "o", "gate_up", "down"):
+                for n in ("qweight", "scales", "zeros", "g_idx"):
+                    assert torch.equal(getattr(getattr(a, layer), n), getattr(getattr(b, layer), n)), (layer, n)
+
+
+def test_rows_of_no_sequence_leave_a_prompt_alone(quantized):  # noqa: F811
+    blocks, rot, _ = quantized
+    table, cu = _int(TABLE), _int([2, 39, 39, 120])
+    outs, caches = [], []
+    for pad in (0.0, float("inf")):
+        x = _stream_of(128, 41)
+        x[:2], x[120:] = 1.0, pad
+        st = G.new_status(_dev())
+        caches.append(_caches(2))
+        outs.append(D.prompt_blocks(x, cu, blocks, rot, caches=caches[-1], table=table, status=st))
+        G.raise_on_status(st, "prompt_blocks")
+    assert torch.equal(outs[0][:120], outs[1][:120]) and torch.isfinite(outs[0]).all()
+    for a, b in zip(*caches):
+        assert all(torch.equal(getattr(a, n), getattr(b, n)) for n in TENSORS)
