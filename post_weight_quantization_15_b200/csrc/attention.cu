@@ -47,7 +47,9 @@
 // used; values past the sequence's end are zeroed in shared memory.  Inside a sequence a
 // causal tile still multiplies weights of 0 with values behind the diagonal, which is
 // exact unless one of them is not finite: a query whose result holds a NaN is therefore
-// computed again one key at a time (seen_row), reading only what it sees.
+// computed again one key at a time (seen_row), reading only what it sees.  Not where its sum of
+// weights is a NaN: that comes from scores it sees, which make its whole row NaN (60,000 queries
+// after a NaN key would each go through all keys by themselves).
 #include <math.h>
 
 #include <climits>
@@ -444,7 +446,7 @@ __device__ __forceinline__ void join_parts(const AttentionArgs& A, AttnSmem<KD>&
       if constexpr (V == 4) *reinterpret_cast<uint2*>(dst + lane * V) = make_uint2(u[0], u[1]);
       else *reinterpret_cast<uint32_t*>(dst + lane * V) = u[0];
     }
-    if (__any_sync(0xffffffffu, nan)) {
+    if (__any_sync(0xffffffffu, nan) && l == l) {
       __syncwarp();                                       // the row's first values before its second
       seen_row<T>(A, w.q0 + me.query, me.head, hk, w.k0, me.seen);
     }
@@ -786,7 +788,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 if (i + 8 < A.head_dim) store8(dst + i + 8, o + 8);
               }
             }
-            unsigned again = __ballot_sync(0xffffffffu, nan && mine);
+            unsigned again = __ballot_sync(0xffffffffu, nan && l == l && mine);
             __syncwarp();                                 // a row's first values before its second
             while (again != 0) {
               const int src = __ffs(again) - 1;
