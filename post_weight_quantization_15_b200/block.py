@@ -242,6 +242,18 @@ def _heads(t: torch.Tensor, dtype, what: str):
     raise ValueError(f"{what} must be a [tokens, heads, head_dim] tensor of type {dtype} with contiguous features")
 
 
+def _written(out: torch.Tensor, like: torch.Tensor, *ins: torch.Tensor):
+    """(token stride, head stride) of a given output: every row has a place of its own, apart from the inputs."""
+    n, h, d, ts, hs = _heads(out, like.dtype, "out")
+    if out.shape != like.shape:
+        raise ValueError("out must have q's shape")
+    if (h > 1 and hs < d) or (n > 1 and ts < d) or \
+            (n > 1 and h > 1 and ts < (h - 1) * hs + d and hs < (n - 1) * ts + d):
+        raise ValueError("out's rows must not overlap")
+    _apart(out, *ins)
+    return ts, hs
+
+
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
               cu_k: Optional[torch.Tensor] = None, causal: bool = True, scale: Optional[float] = None,
               out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -267,16 +279,11 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Ten
     _ints(cu_q, cu_q.shape, "cu_q")
     if cu_k is not cu_q:
         _ints(cu_k, cu_q.shape, "cu_k")
+    ot, oh = (hq * d, d) if out is None else _written(out, q, q, k, v)
     _status_ok(status)
     with _Launching(stream, q, k, v, cu_q, cu_k, out, status) as s:
         if out is None:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
-            ot, oh = hq * d, d
-        else:
-            _, _, _, ot, oh = _heads(out, dt, "out")
-            if out.shape != q.shape:
-                raise ValueError("out must have q's shape")
-            _apart(out, q, k, v)
         rc = lib().gptq_attention(q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, _DTYPE_CODE[dt],
                                   cu_q.data_ptr(), cu_k.data_ptr(), cu_q.numel() - 1, nq, nk, hq, hk, d,
                                   d ** -0.5 if scale is None else float(scale), bool(causal), out.data_ptr(), ot, oh,
@@ -409,6 +416,9 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, table: torch.Tensor, lengths
         raise ValueError("q must have the cache's head size and a multiple of its heads")
     _ints(lengths, (count,), "lengths")
     _table(table, count)
+    ot, oh = (hq * d, d) if out is None else _written(out, q, q)
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
     _status_ok(status)
     width = table.shape[1]
     with _Launching(stream, cache.k_codes, cache.k_params, cache.v_codes, cache.v_params, q, table, lengths, ws, out,
@@ -418,12 +428,6 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, table: torch.Tensor, lengths
                            q.device)
         if out is None:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
-            ot, oh = hq * d, d
-        else:
-            _, _, _, ot, oh = _heads(out, dt, "out")
-            if out.shape != q.shape:
-                raise ValueError("out must have q's shape")
-            _apart(out, q)
         rc = lib().gptq_kv4_attention(ctypes.byref(desc), q.data_ptr(), qt, qh, _DTYPE_CODE[dt], count, hq,
                                       table.data_ptr(), width, lengths.data_ptr(),
                                       d ** -0.5 if scale is None else float(scale), out.data_ptr(), ot, oh,
