@@ -434,6 +434,8 @@ GPTQ_API int gptq_residual_add(const void* X, const float* Y, int64_t count, voi
  * of quantized blocks) and for decoding single tokens beside gptq_qmatvec.  Activations are
  * token-major here: [tokens, features] with contiguous features.  Types F32, F16, BF16
  * where "any" is said.  tokens, count or total_q of 0 is a no-op.  d_status may be NULL.
+ * GPTQ_ERR_UNSUPPORTED from 2^31 - 2048 tokens of gptq_rope_qkv, rows of gptq_attention and
+ * positions of a sequence (width . page_size) of gptq_kv4_attention on.
  *
  * gptq_add_norm - the norms around a block with the residual addition between them:
  *     Xn = round(X + alpha . gate . N(Y; post_weight, post_bias))      h = round(N(Xn; weight, bias))

@@ -36,6 +36,10 @@ bool valid_gs(int gs) { return gs == -1 || gs == 32 || gs == 64 || gs == 128; }
 bool valid_dtype(int t) { return t == GPTQ_F32 || t == GPTQ_F16 || t == GPTQ_BF16; }
 bool valid_dtype16(int t) { return t == GPTQ_F16 || t == GPTQ_BF16; }
 
+// What the kernels' 32-bit rows and tiles count up to: they step past a tensor's end by less than SLACK.
+constexpr int SLACK = 2048;
+constexpr int MOST_ROWS = INT32_MAX - SLACK;
+
 // A [tokens, heads, head_dim] operand of 16-bit values read or written in 16-byte pieces.
 bool valid_heads(const void* p, int64_t token_stride, int64_t head_stride) {
   return p != nullptr && aligned(p, 16) && token_stride >= 0 && head_stride >= 0 && token_stride % 8 == 0 &&
@@ -339,7 +343,7 @@ int gptq_rope_qkv(const void* X, int x_dtype, int64_t ld, const float* bias, con
   if (X == nullptr || q == nullptr || k == nullptr || v == nullptr) return GPTQ_ERR_INVALID_ARG;
   if (rot > 0 && (cos == nullptr || sin == nullptr || max_pos < 1)) return GPTQ_ERR_INVALID_ARG;
   const int64_t cols = ((int64_t)heads_q + 2 * (int64_t)heads_kv) * head_dim;
-  if (cols > (1 << 30)) return GPTQ_ERR_UNSUPPORTED;
+  if (cols > (1 << 30) || tokens > MOST_ROWS) return GPTQ_ERR_UNSUPPORTED;
   if (ld < cols) return GPTQ_ERR_INVALID_ARG;
   return launch_rope_qkv(X, x_dtype, ld, bias, cos, sin, max_pos, rot, interleaved, positions, tokens, heads_q,
                          heads_kv, head_dim, out_dtype, q, k, v, d_status, as_stream(stream));
@@ -353,7 +357,8 @@ int gptq_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
   if (count < 0 || total_q < 0 || total_k < 0 || heads_q < 1 || heads_kv < 1 || heads_q % heads_kv != 0)
     return GPTQ_ERR_INVALID_ARG;
   if (!valid_dtype16(dtype) || head_dim < 1 || !(scale == scale)) return GPTQ_ERR_INVALID_ARG;
-  if (head_dim % 8 != 0 || head_dim > 128 || heads_q > 65535) return GPTQ_ERR_UNSUPPORTED;
+  if (head_dim % 8 != 0 || head_dim > 128 || heads_q > 65535 || total_q > MOST_ROWS || total_k > MOST_ROWS)
+    return GPTQ_ERR_UNSUPPORTED;
   if (count == 0 || total_q == 0) return GPTQ_OK;
   if (cu_q == nullptr || cu_k == nullptr || !valid_heads(q, q_token_stride, q_head_stride) ||
       !valid_heads(o, o_token_stride, o_head_stride))
@@ -417,7 +422,7 @@ int gptq_kv4_attention(const gptq_kv4_cache* cache, const void* q, int64_t q_tok
   if (table == nullptr || width < 1 || lengths == nullptr || !valid_heads(q, q_token_stride, q_head_stride) ||
       !valid_heads(o, o_token_stride, o_head_stride))
     return GPTQ_ERR_INVALID_ARG;
-  if ((int64_t)width * C.page_size > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
+  if ((int64_t)width * C.page_size > MOST_ROWS) return GPTQ_ERR_UNSUPPORTED;
   if (ws == nullptr || !aligned(ws, 256) ||
       ws_bytes < kv4_attention_ws_bytes(count, heads_q, C.heads, C.head_dim, (int64_t)width * C.page_size))
     return GPTQ_ERR_WORKSPACE;

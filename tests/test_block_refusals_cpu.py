@@ -1,5 +1,7 @@
 """What the decoder-block operators refuse before anything is launched: outputs and workspaces that do not
 have a place of their own for every value, and sizes that do not fit the arithmetic of the kernels."""
+import ctypes
+
 import pytest
 
 import post_weight_quantization_15_b200 as G
@@ -47,3 +49,38 @@ def test_workspaces_that_are_not_as_long_as_they_say():
     for ws in (_cpu(1).expand(10 ** 9), _cpu(100, 2)[:, 0]):
         with pytest.raises(ValueError, match="ws"):
             G.kv4_attention(q, CACHE, _i(0, 0, 0).view(3, 1), _i(1, 1, 1), ws=ws)
+
+
+# --------------------------------------------------------------------------- #
+# The C ABI near 2^31 (pointers that are never used: without a GPU nothing is launched)
+# --------------------------------------------------------------------------- #
+FAKE = ctypes.c_void_p(256)
+LIMIT = 2 ** 31 - 2048                                           # the first size that is refused
+UNSUPPORTED = -2
+
+
+def test_rows_of_attention_near_the_end_of_32_bits():
+    """Tiles reach past the last row: 128 rows, times the eight blocks that may share them."""
+    def call(total_q, total_k):
+        return G.lib().gptq_attention(FAKE, 64, 64, FAKE, 64, 64, FAKE, 64, 64, 2, FAKE, FAKE, 1, total_q, total_k, 1, 1,
+                                      64, 0.1, 1, FAKE, 64, 64, None, None)
+    for n in (LIMIT, 2 ** 31 - 1):
+        assert call(n, 5) == UNSUPPORTED and call(5, n) == UNSUPPORTED
+
+
+def test_tokens_of_rope_near_the_end_of_32_bits():
+    """Blocks of up to 256 tokens count past the last one."""
+    def call(tokens):
+        return G.lib().gptq_rope_qkv(FAKE, 0, 512, None, FAKE, FAKE, 8, 64, 0, None, tokens, 4, 2, 64, 2, FAKE, FAKE,
+                                     FAKE, None, None)
+    assert call(LIMIT) == UNSUPPORTED and call(2 ** 31 - 1) == UNSUPPORTED
+
+
+def test_positions_of_kv4_attention_near_the_end_of_32_bits():
+    """A length's tiles of 32 are counted from length + 31."""
+    desc = G.gptq._KV4(256, 256, 256, 256, 4, 16, 2, 64, 32)
+
+    def call(width):
+        return G.lib().gptq_kv4_attention(ctypes.byref(desc), FAKE, 64, 64, 2, 1, 4, FAKE, width, FAKE, 0.1, FAKE, 64, 64,
+                                          FAKE, 1 << 40, None, None)
+    assert call(LIMIT // 16) == UNSUPPORTED and call((2 ** 31 - 1) // 16) == UNSUPPORTED
