@@ -24,6 +24,11 @@ import torch
 from .gptq import _DTYPE_CODE, _KV4, OK, GptqError, _check, _require_cuda, lib, workspace
 
 _16BIT = (torch.float16, torch.bfloat16)
+_INT_MAX = 2 ** 31 - 1        # the C ABI's counts; ctypes would cut a larger one off without a word
+
+
+def _too_large(what: str):
+    return ValueError(f"{what}: sizes from 2^31 on are not supported")
 
 
 class _Launching:
@@ -93,6 +98,8 @@ def _apart(out: Optional[torch.Tensor], *ins: Optional[torch.Tensor]):
 def _rows(t: torch.Tensor, tokens: int, d: int, what: str):
     if t.dtype in _DTYPE_CODE and t.shape == (tokens, d):
         if t.is_contiguous() or ((d == 1 or t.stride(1) == 1) and (tokens == 1 or t.stride(0) >= d)):
+            if tokens > _INT_MAX or d > _INT_MAX:
+                raise _too_large(what)
             return
     raise ValueError(f"{what} must be an fp32/fp16/bf16 [{tokens}, {d}] tensor with contiguous rows")
 
@@ -110,6 +117,8 @@ def _ld(t: Optional[torch.Tensor], d: int) -> int:
 def _ints(t: torch.Tensor, shape, what: str):
     if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)}")
+    if shape[0] > _INT_MAX:
+        raise _too_large(what)
 
 
 # --------------------------------------------------------------------------- #
@@ -236,6 +245,8 @@ def _heads(t: torch.Tensor, dtype, what: str):
         n, h, d = t.shape
         ts, hs, fs = t.stride()
         if h > 0 and (fs == 1 or d <= 1):
+            if n > _INT_MAX or h > _INT_MAX or d > _INT_MAX:
+                raise _too_large(what)
             if h == 1:
                 hs = d
             return n, h, d, ts if n > 1 else h * hs, hs
@@ -319,6 +330,8 @@ def _cache(c: KV4Cache) -> _KV4:
         raise ValueError("k_codes must be int32 [pages, heads, page_size, head_dim / 8]")
     shape = kc.shape
     pages, heads, page, words = shape
+    if pages > _INT_MAX or heads > _INT_MAX or page > _INT_MAX:
+        raise _too_large("k_codes")
     d = words * 8
     if group < 1 or d % group:
         raise ValueError("group must divide head_dim")
@@ -334,6 +347,8 @@ def _cache(c: KV4Cache) -> _KV4:
 def _table(table: torch.Tensor, count: int):
     if table.dim() != 2 or table.dtype != torch.int32 or table.shape[0] != count or not table.is_contiguous():
         raise ValueError("table must be a contiguous int32 tensor [sequences, pages of a sequence]")
+    if table.shape[1] > _INT_MAX:
+        raise _too_large("table")
 
 
 def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, cu: torch.Tensor,
@@ -378,6 +393,8 @@ def kv4_read(cache: KV4Cache, table: torch.Tensor, cu: torch.Tensor, tokens: int
     count = cu.numel() - 1
     if count < 0 or tokens < 0:
         raise ValueError("cu must be int32 [sequences + 1] and tokens not negative")
+    if tokens > _INT_MAX:
+        raise _too_large("tokens")
     _ints(cu, (count + 1,), "cu")
     if start is not None:
         _ints(start, (count,), "start")

@@ -84,3 +84,37 @@ def test_positions_of_kv4_attention_near_the_end_of_32_bits():
         return G.lib().gptq_kv4_attention(ctypes.byref(desc), FAKE, 64, 64, 2, 1, 4, FAKE, width, FAKE, 0.1, FAKE, 64, 64,
                                           FAKE, 1 << 40, None, None)
     assert call(LIMIT // 16) == UNSUPPORTED and call((2 ** 31 - 1) // 16) == UNSUPPORTED
+
+
+# --------------------------------------------------------------------------- #
+# Sizes that the ABI's ints would cut off (2^32 + 5 would become 5)
+# --------------------------------------------------------------------------- #
+BIG = 2 ** 32 + 5
+
+
+def _meta(*shape, dtype=torch.float16):
+    return torch.empty(*shape, dtype=dtype, device="meta")
+
+
+I32 = torch.int32
+
+
+@pytest.mark.parametrize("call", [
+    lambda: G.add_norm(_meta(BIG, 8), _meta(8)),
+    lambda: G.add_norm(_meta(1, BIG), _meta(BIG)),
+    lambda: G.rope_qkv(_meta(BIG, 24), None, None, 1, 1, 8),
+    lambda: G.rope_qkv(_meta(1, (BIG + 2) * 2), None, None, BIG, 1, 2),
+    lambda: G.attention(_meta(BIG, 1, 8), _meta(4, 1, 8), _meta(4, 1, 8), _meta(2, dtype=I32)),
+    lambda: G.attention(_meta(4, 1, 8), _meta(BIG, 1, 8), _meta(BIG, 1, 8), _meta(2, dtype=I32)),
+    lambda: G.attention(_meta(4, 1, 8), _meta(4, 1, 8), _meta(4, 1, 8), _meta(BIG, dtype=I32)),
+    lambda: G.kv4_append(CACHE, _meta(BIG, 2, 64), _meta(BIG, 2, 64), _meta(1, 1, dtype=I32), _meta(2, dtype=I32),
+                         _meta(1, dtype=I32)),
+    lambda: G.kv4_append(CACHE, _meta(4, 2, 64), _meta(4, 2, 64), _meta(1, BIG, dtype=I32), _meta(2, dtype=I32),
+                         _meta(1, dtype=I32)),
+    lambda: G.kv4_read(CACHE, _meta(1, 1, dtype=I32), _meta(2, dtype=I32), BIG),
+    lambda: G.kv4_attention(_meta(BIG, 2, 64), CACHE, _meta(BIG, 1, dtype=I32), _meta(BIG, dtype=I32)),
+    lambda: G.kv4_attention(_meta(1, 2, 64), CACHE, _meta(1, BIG, dtype=I32), _meta(1, dtype=I32)),
+])
+def test_sizes_beyond_the_abi(call):
+    with pytest.raises(ValueError, match="2\\^31"):
+        call()
