@@ -169,7 +169,9 @@ __global__ void __launch_bounds__(256) qmatvec_kernel(const int32_t* qweight, co
                                                       const uint16_t* zeros, const int32_t* g_idx, int n, int out,
                                                       int groups, const TX* X, const int32_t* xperm, int m_real,
                                                       int ldx, float* part, int32_t* st) {
-  if (has_error(st)) return;
+  // one answer for the block: other blocks of this launch may record an error meanwhile, and warps
+  // that left one by one would leave the others shared memory that nobody has written
+  if (__syncthreads_or(threadIdx.x == 0 && has_error(st))) return;
   constexpr int PER = 32 / BITS;
   constexpr int kc = qmv_kc(M);
   constexpr int QMV_MAXG = qmv_maxg(M);

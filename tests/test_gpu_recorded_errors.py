@@ -271,3 +271,30 @@ def test_rope_qkv_beside_a_bad_position(tokens, hq, hk, d, dt, bad):
         assert code == INVALID and token in (1, tokens - 2)
         for x, y in zip(got, want):
             assert torch.equal(x, y)
+
+
+# --------------------------------------------------------------------------- #
+# qmatvec: 512 blocks that all find the bad group index while others start
+# --------------------------------------------------------------------------- #
+@pytest.mark.parametrize("rows", [1, 4])
+def test_qmatvec_records_a_bad_group_index(rows):
+    rng = np.random.default_rng(10)
+    out, n, groups = 65536, 1024, 8
+    q = G.QuantizedLayer(torch.from_numpy(rng.integers(-2 ** 31, 2 ** 31, (n // 8, out), dtype=np.int32)).to(_dev()),
+                         (_rand(rng, (groups, out), FF).abs() + 0.5).to(HF), torch.full((groups, out), 8.0, dtype=HF,
+                                                                                      device=_dev()),
+                         torch.arange(n, dtype=torch.int32, device=_dev()) // 128, None, None, 4, 128, False)
+    X = _rand(rng, (rows, n), BF)
+    want = G.qmatvec(q, X)
+    good = q.g_idx.clone()
+    for bad in (groups, -1, 2 ** 31 - 1):
+        q.g_idx[5] = bad
+        st = G.new_status(_dev())
+        for _ in range(5):
+            G.status_reset(st)
+            G.qmatvec(q, X, st)
+            assert G.status_read(st) == (INVALID, 5)
+    q.g_idx.copy_(good)
+    G.status_reset(st)
+    assert torch.equal(G.qmatvec(q, X, st), want)
+    assert G.status_read(st)[0] == 0
