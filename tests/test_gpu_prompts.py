@@ -192,3 +192,24 @@ def test_rows_of_no_sequence_leave_a_prompt_alone(quantized):  # noqa: F811
     assert torch.equal(outs[0][:120], outs[1][:120]) and torch.isfinite(outs[0]).all()
     for a, b in zip(*caches):
         assert all(torch.equal(getattr(a, n), getattr(b, n)) for n in TENSORS)
+
+
+def test_a_captured_prompt(quantized):  # noqa: F811
+    """Defaults for start, positions and status, replayed on another batch of the same shape."""
+    blocks, rot, _ = quantized
+    table, cu = _int(TABLE), _int([0, 37, 37, 127])
+    xs = [_rows(127, 42), _rows(127, 43)]
+    want, kept = [], []
+    for x in xs:
+        kept.append(_caches(2))
+        want.append(D.prompt_blocks(x, cu, blocks, rot, caches=kept[-1], table=table))
+    caches, x_in = _caches(2), xs[0].clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = D.prompt_blocks(x_in, cu, blocks, rot, caches=caches, table=table)
+    for x, w, k in zip(xs, want, kept):
+        x_in.copy_(x)
+        g.replay()
+        assert torch.equal(out, w)
+        for a, b in zip(caches, k):
+            assert all(torch.equal(getattr(a, n), getattr(b, n)) for n in TENSORS)
