@@ -26,9 +26,9 @@
 //
 // 16 x 2048 causal tokens x 32 heads of 128: 795 us with waits polled by one lane of a warp and
 // passed on, 730 polled by all lanes, 700 with the products issued by one elected thread, 680
-// with the weights handed over in two parts, 615 with blocks that stay (895 TFLOP/s); packed
-// sequences up to 6007, 64/8 heads: 1245, 1126, 1074, 1040, 1005 us, and 934 with eight heads to a
-// tile (1067 TFLOP/s).  What bounds it: the chain of one tile, about 2300 cycles of softmax (1024
+// with the weights handed over in two parts, 627 with blocks that stay (877 TFLOP/s); packed
+// sequences up to 6007, 64/8 heads: 1245, 1126, 1074, 1040, 1005 us, and 942 with eight heads to a
+// tile (1059 TFLOP/s).  What bounds it: the chain of one tile, about 2300 cycles of softmax (1024
 // of them exponentials) and 1500 for 16 products of 64 cycles and their latencies, of which the
 // other tile hides half.  Tried and not kept: a quarter of the exponentials as polynomials on
 // the fma units (slower or even), two threads per query (6% slower: the exchange of maxima),
@@ -840,7 +840,7 @@ int64_t most_pairs(const AttentionArgs& A) {
 // Query heads of one k/v head share tiles (2^packed of them, their rows the queries' heads in
 // turn): until an average sequence fills a tile, and on while there is work for every SM four
 // times over (a pair of tiles then spans fewer queries, whose causal limits are closer: packed
-// sequences, 64/8 heads: 1005 us with none, 934 with eight; 64 queries, 32/8 heads: 8 us with
+// sequences, 64/8 heads: 1005 us with none, 942 with eight; 64 queries, 32/8 heads: 8 us with
 // none or two, 11 with four, whose blocks are too few).
 int packed_heads(AttentionArgs A) {
   const int per = A.heads_q / A.heads_kv;

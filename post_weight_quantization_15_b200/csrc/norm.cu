@@ -26,7 +26,7 @@
 // ends.  (fp32 streams read single values side by side.)  32768 rows of 4096, bf16 with fp32
 // Y: 203 us, 1.01 of the measured copy bandwidth.  2039 rows of 5125, fp16, norms on both
 // sides: 117 us with everything in registers that spilled, 65 with single values, 57 shifted, 51
-// with three blocks per SM; about 1400 instructions per warp and row bound it.
+// with three blocks per SM; about 1480 instructions per warp and row bound it.
 #include "common.cuh"
 #include "internal.h"
 #include "vec_io.cuh"
