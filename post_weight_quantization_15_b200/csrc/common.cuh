@@ -47,7 +47,8 @@ __device__ __forceinline__ void set_own_error(int32_t* st, int launch, int code,
 
 // An error that was there before the launch.  Where threads of a block depend on one another
 // one thread asks for all.  From here on the error is nobody's own: a graph that holds the call
-// which recorded it stops there too when it is replayed.
+// which recorded it (under the same number in every replay) stops there too when it is replayed.
+// (Replays of a graph of that call alone, which nobody else has seen the error of, go on.)
 __device__ __forceinline__ bool stopped(int32_t* st, int launch) {
   if (!has_error(st)) return false;
   __threadfence();

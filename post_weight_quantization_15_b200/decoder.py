@@ -155,6 +155,9 @@ def quantize_decoder_blocks(X0: torch.Tensor, cu: torch.Tensor, blocks: Sequence
 
 def _positions(cu: torch.Tensor, start: Optional[torch.Tensor], tokens: int) -> torch.Tensor:
     """Each row's position inside its sequence, behind start[b]; 0 for a row of no sequence."""
+    B._ints(cu, (cu.numel(),), "cu")
+    if start is not None:
+        B._ints(start, (max(0, cu.numel() - 1),), "start")
     if cu.numel() < 2:
         return torch.zeros(tokens, dtype=torch.int32, device=cu.device)
     t = torch.arange(tokens, dtype=torch.int32, device=cu.device)
@@ -239,7 +242,6 @@ def prompt_blocks(X: torch.Tensor, cu: torch.Tensor, blocks: Sequence[QuantizedB
     if caches is not None and start is None:
         start = torch.zeros(cu.numel() - 1, dtype=torch.int32, device=X.device)
     if positions is None and r.cos is not None:
-        B._ints(cu, (cu.numel(),), "cu")
         positions = _positions(cu, start, X.shape[0])
     for i, b in enumerate(blocks):
         X, h = B.add_norm(X, b.norm_attn, Y=y, eps=b.eps, status=status)

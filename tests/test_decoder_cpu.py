@@ -58,3 +58,12 @@ def test_rows_of_no_sequence_are_cleared():
     assert (D._without_strays(x, _i(0)) == 0).all() and (D._without_strays(x, _i(2, 2)) == 0).all()
     with pytest.raises(ValueError, match="cu"):
         D._without_strays(x, _i(0, 3).long())
+
+
+def test_positions_refuse_a_start_of_another_length():
+    """Also where no block is there to check it: rows would be looked up past its end."""
+    for start in (_i(0, 0, 0), _i(0), _i(0, 0).long()):
+        with pytest.raises(ValueError, match="start"):
+            D._positions(_i(0, 3, 5), start, 5)
+    with pytest.raises(ValueError, match="cu"):
+        D._positions(_i(0, 3, 5).long(), None, 5)
